@@ -339,8 +339,10 @@ def _prepare_adamw(c, seed):
     names = [k for k in ("master", "exp_avg", "exp_avg_sq", "exp_rms") if s.get(k) is not None]
     parts = {k: cut(s[k]) for k in names}
     parts.update({k: cutb(s[k]) for k in ("exp_avg_scale", "exp_rms_scale") if k in s})
-    s["tensors"] = {"params": cut(s["param"]), "grads": cut(s["grad"]), "weight_decay": decay,
-                    "states": [{k: v[i] for k, v in parts.items()} for i in range(len(sizes))]}
+    states = [{k: v[i] for k, v in parts.items()} for i in range(len(sizes))]
+    if own:  # the list of tensors, checked once, as a program keeps it over the steps
+        import rl_policy_gradient_amd as plp
+        s["table"] = plp.adamw_table(cut(s["param"]), cut(s["grad"]), states, weight_decay=decay)
     return s
 
 
@@ -393,9 +395,8 @@ def _adamw_plain(s):
 def _adamw_own(s):
     import rl_policy_gradient_amd as plp
     s["step"] += 1
-    t = s["tensors"]
-    plp.adamw_step(t["params"], t["grads"], t["states"], lr=ADAM["lr"], betas=(ADAM["beta1"], ADAM["beta2"]),
-                   eps=ADAM["eps"], weight_decay=t["weight_decay"], step=s["step"], grad_scale=s["grad_scale"])
+    plp.adamw_step(s["table"], lr=ADAM["lr"], step=s["step"], betas=(ADAM["beta1"], ADAM["beta2"]), eps=ADAM["eps"],
+                   grad_scale=s["grad_scale"])
     return _adamw_outputs(s)
 
 
