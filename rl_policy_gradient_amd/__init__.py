@@ -16,6 +16,8 @@ import torch
 
 from . import _abi
 from ._abi import METRIC_NAMES, PlpError  # noqa: F401
+from ._marshal import _check_vec, _dtype_code, _ptr, _stream, _workspace
+from .operators import layer_norm_bwd, layer_norm_fwd
 
 __all__ = [
     "fused_lmhead_policy_loss_fwd_bwd",
@@ -26,6 +28,8 @@ __all__ = [
     "prepare_weight",
     "prepared_weight_size",
     "workspace_size",
+    "layer_norm_fwd",
+    "layer_norm_bwd",
     "METRIC_NAMES",
     "PlpError",
 ]
@@ -33,44 +37,6 @@ __all__ = [
 _LOSS = {"gmpo": _abi.LOSS_GMPO, "gspo_token": _abi.LOSS_GSPO_TOKEN, "grpo": _abi.LOSS_GRPO,
          "bnpo": _abi.LOSS_BNPO, "dapo": _abi.LOSS_DAPO}
 _RED = {"seq_mean": _abi.REDUCE_SEQ_MEAN, "token_sum": _abi.REDUCE_TOKEN_SUM}
-
-
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise ValueError("plp runs on the GPU only: got a CPU tensor")
-    if not t.is_contiguous():
-        raise ValueError("plp needs contiguous tensors")
-    return t.data_ptr()
-
-
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return _abi.DTYPE_F32
-    if t.dtype == torch.bfloat16:
-        return _abi.DTYPE_BF16
-    raise ValueError(f"unsupported dtype {t.dtype}: float32 or bfloat16")
-
-
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
-    if workspace is not None:
-        if workspace.numel() * workspace.element_size() < nbytes:
-            raise ValueError(f"workspace too small: need {nbytes} bytes")
-        return workspace
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-
-
-def _check_vec(t, n, dtype, name):
-    if t is None:
-        return None
-    if t.numel() != n or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {n} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
-    return t
 
 
 def _mask_u8(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:

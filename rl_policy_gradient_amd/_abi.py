@@ -93,6 +93,9 @@ class PlpError(RuntimeError):
         self.code = code
 
 
+# entry points added to ABI version 5 after its first libraries
+_LATER = ("plp_layer_norm_fwd", "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd")
+
 _lib = None
 
 
@@ -104,6 +107,10 @@ def lib() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m rl_policy_gradient_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
+    missing = [n for n in _LATER if not hasattr(L, n)]
+    if missing:
+        raise ImportError(f"{LIB_PATH} lacks {', '.join(missing)}: rebuild it with "
+                          "`python -m rl_policy_gradient_amd.build`")
     sz = ctypes.c_size_t
     P = ctypes.POINTER
     L.plp_abi_version.restype = ctypes.c_int
@@ -125,6 +132,10 @@ def lib() -> ctypes.CDLL:
     L.plp_policy_loss_from_logprobs.argtypes = [P(PlpArgs), _vp, _vp, P(PlpOutputs), _vp, sz, _vp]
     L.plp_prepared_weight_size.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P(sz)]
     L.plp_prepare_weight.argtypes = [_vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp, sz, _vp]
+    i32, i64, f64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+    L.plp_layer_norm_fwd.argtypes = [_vp, _vp, _vp, i64, i32, i32, i32, f64, _vp, _vp, _vp, _vp]
+    L.plp_layer_norm_bwd_workspace_size.argtypes = [i64, i32, i32, P(sz)]
+    L.plp_layer_norm_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, i64, i32, i32, i32, _vp, _vp, _vp, _vp, sz, _vp]
     L.plp_profile_start.argtypes = [ctypes.c_int32]
     L.plp_profile_stop.argtypes = [P(ctypes.c_double), P(ctypes.c_int32)]
     L.plp_profile_stop_n.argtypes = [P(ctypes.c_double), P(ctypes.c_int32), ctypes.c_int32]
@@ -135,7 +146,8 @@ def lib() -> ctypes.CDLL:
                  "plp_selective_entropy", "plp_selective_entropy_prepared_workspace_size",
                  "plp_selective_entropy_prepared", "plp_entropy_quantile_mask_workspace_size", "plp_entropy_quantile_mask",
                  "plp_entropy_quantile_mask_noalloc", "plp_prepared_weight_size", "plp_prepare_weight",
-                 "plp_policy_loss_workspace_size", "plp_policy_loss_from_logprobs"):
+                 "plp_policy_loss_workspace_size", "plp_policy_loss_from_logprobs", "plp_layer_norm_fwd",
+                 "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd"):
         getattr(L, name).restype = ctypes.c_int
     if L.plp_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI version {L.plp_abi_version()}, this binding {ABI_VERSION}: "

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/plp.h"
+#include "api.h"
 #include "common.h"
 
 using namespace plp;
@@ -42,7 +43,9 @@ namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int code, const char* fmt, ...) {
+}  // namespace
+
+int plp::fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -52,19 +55,26 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-int ok() {
+int plp::ok() {
   g_last_error.clear();
   return PLP_OK;
 }
 
-constexpr size_t kAlign = 256;
+int plp::check_ws(void* ws, size_t have, size_t need) {
+  if (need > have) return fail(PLP_E_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", have, need);
+  if (need > 0 && ws == nullptr) return fail(PLP_E_WORKSPACE, "workspace is NULL");
+  if (((uintptr_t)ws) % kAlign != 0) return fail(PLP_E_WORKSPACE, "workspace must be 256-byte aligned");
+  return PLP_OK;
+}
+
+namespace {
+
 constexpr int kBQ = 64, kBK = 32;
 constexpr int kMaxSplits = 64;
 // Rows of the second forward pass over flagged rows per call of the sweep
 // (more flagged rows than this are recomputed by the merge on the vector
 // ALU); its statistics and accumulator hold compact_rows_needed rows.
 constexpr int64_t kFlagCap = 32768;
-constexpr int64_t kMaxRows = (int64_t)1 << 31;
 // plp_args as of ABI version 1 (fields up to chunk_sequences); later fields
 // read as their defaults when struct_size ends before them.
 constexpr size_t kArgsV1Size = offsetof(plp_args, global_tokens);
@@ -85,31 +95,14 @@ const void* weight_prepared(const plp_args* a) {
   return a->struct_size >= offsetof(plp_args, weight_prepared) + sizeof(void*) ? a->weight_prepared : nullptr;
 }
 
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
 // Rows of stats / O a compacted accumulator pass over at most `cap` listed
 // rows can use: the largest splits x row stride the sweep picks for any
 // count up to cap (both depend on the count through its 64-row blocks only).
 int64_t compact_rows_needed(int64_t cap, int V, int max_splits) { return 64 * forward_blocks_max(cap, V, max_splits); }
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Sequential carving of the caller's workspace.
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base((char*)b) {}
-  template <typename T>
-  T* take(size_t count) {
-    if (count == 0) return nullptr;
-    T* p = base ? (T*)(base + off) : nullptr;
-    off += align_up(count * sizeof(T));
-    return p;
-  }
-};
-
 bool mfma_eligible(int dtype, int H) { return dtype == PLP_DTYPE_BF16 && H % 128 == 0 && H >= 128 && H <= 896; }
 bool generic_eligible(int H) { return H >= 1 && H <= 4096; }
-size_t esize(int dtype) { return dtype == PLP_DTYPE_F32 ? 4 : 2; }
 
 // Vocabulary splits of the forward sweep over all rows of a chunk
 // (forward_splits); the generic path does not split.
@@ -261,19 +254,6 @@ hipEvent_t* prof_slot(int k) {
   g_prof.kind[g_prof.used] = k;
   ++g_prof.used;
   return p;
-}
-
-#define HIP_TRY(expr)                                                                   \
-  do {                                                                                  \
-    hipError_t e_ = (expr);                                                             \
-    if (e_ != hipSuccess) return fail(PLP_E_HIP, "%s: %s", #expr, hipGetErrorString(e_)); \
-  } while (0)
-
-int check_ws(void* ws, size_t have, size_t need) {
-  if (need > have) return fail(PLP_E_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", have, need);
-  if (need > 0 && ws == nullptr) return fail(PLP_E_WORKSPACE, "workspace is NULL");
-  if (((uintptr_t)ws) % kAlign != 0) return fail(PLP_E_WORKSPACE, "workspace must be 256-byte aligned");
-  return PLP_OK;
 }
 
 // Checks shared by the fused call and the loss-only call. `pointers`: also

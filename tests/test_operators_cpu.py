@@ -1,0 +1,101 @@
+"""The operators around the fused loss without a GPU: sizes and refusals. Every
+call here is answered by the host checks before any launch; the pointers are
+made up and never followed."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+abi = pytest.importorskip("rl_policy_gradient_amd._abi")
+
+
+def _lib():
+    if not os.path.exists(abi.LIB_PATH):
+        pytest.skip("libplp.so not built")
+    return abi.lib()
+
+
+def _err():
+    return _lib().plp_last_error().decode()
+
+
+X, W, B, Y, M, R, G, WS = (0x10000000 * (i + 1) for i in range(8))  # far apart: nothing overlaps
+
+
+def norm_fwd(**kw):
+    a = dict(x=X, w=W, b=B, N=8, H=64, dtype=abi.DTYPE_BF16, rms=0, eps=1e-5, y=Y, mean=M, rstd=R)
+    a.update(kw)
+    return _lib().plp_layer_norm_fwd(a["x"], a["w"], a["b"], a["N"], a["H"], a["dtype"], a["rms"], a["eps"], a["y"],
+                                     a["mean"], a["rstd"], None)
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(N=-1), abi.PLP_E_INVALID, "N=-1"),
+    (dict(N=1 << 31), abi.PLP_E_INVALID, "N="),
+    (dict(H=0), abi.PLP_E_INVALID, "H must"),
+    (dict(H=65537), abi.PLP_E_UNSUPPORTED, "H=65537"),
+    (dict(dtype=2), abi.PLP_E_INVALID, "dtype"),
+    (dict(eps=-1.0), abi.PLP_E_INVALID, "eps"),
+    (dict(eps=float("nan")), abi.PLP_E_INVALID, "eps"),
+    (dict(w=None), abi.PLP_E_INVALID, "weight"),
+    (dict(x=None), abi.PLP_E_INVALID, "x and y"),
+    (dict(y=None), abi.PLP_E_INVALID, "x and y"),
+    (dict(rms=1), abi.PLP_E_INVALID, "mean_out"),
+    (dict(x=X + 1), abi.PLP_E_INVALID, "aligned"),
+    (dict(y=X), abi.PLP_E_INVALID, "overlap"),
+    (dict(y=X + 8 * 64 * 2 - 2), abi.PLP_E_INVALID, "overlap"),
+    (dict(y=W - 2), abi.PLP_E_INVALID, "overlap"),
+])
+def test_norm_forward_refuses(kw, code, msg):
+    assert norm_fwd(**kw) == code
+    assert msg in _err()
+
+
+def norm_bwd(**kw):
+    a = dict(gy=Y, x=X, w=W, mean=M, rstd=R, N=8, H=64, dtype=abi.DTYPE_F32, rms=0, gx=G, gw=B, gb=B + 4096, ws=WS,
+             n=1 << 20)
+    a.update(kw)
+    return _lib().plp_layer_norm_bwd(a["gy"], a["x"], a["w"], a["mean"], a["rstd"], a["N"], a["H"], a["dtype"],
+                                     a["rms"], a["gx"], a["gw"], a["gb"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(N=-1), abi.PLP_E_INVALID, "N=-1"),
+    (dict(H=-3), abi.PLP_E_INVALID, "H must"),
+    (dict(gy=None), abi.PLP_E_INVALID, "required"),
+    (dict(rstd=None), abi.PLP_E_INVALID, "required"),
+    (dict(mean=None), abi.PLP_E_INVALID, "required"),
+    (dict(w=None), abi.PLP_E_INVALID, "weight"),
+    (dict(gx=X + 2), abi.PLP_E_INVALID, "aligned"),
+    (dict(gx=Y), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(gw=W), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(gb=B), abi.PLP_E_INVALID, "overlap each other"),
+    (dict(n=16), abi.PLP_E_WORKSPACE, "too small"),
+    (dict(ws=None), abi.PLP_E_WORKSPACE, "NULL"),
+    (dict(ws=WS + 128), abi.PLP_E_WORKSPACE, "aligned"),
+])
+def test_norm_backward_refuses(kw, code, msg):
+    assert norm_bwd(**kw) == code
+    assert msg in _err()
+
+
+def test_norm_of_nothing_and_workspace():
+    assert norm_fwd(N=0, x=None, y=None) == abi.PLP_OK
+    L, n, m = _lib(), ctypes.c_size_t(), ctypes.c_size_t()
+    for N, H in ((0, 5), (1, 1), (65536, 896), ((1 << 31) - 1, 65536)):
+        assert L.plp_layer_norm_bwd_workspace_size(N, H, abi.DTYPE_BF16, ctypes.byref(n)) == 0
+        assert n.value >= 2 * H * 4 and n.value % 256 == 0
+        assert L.plp_layer_norm_bwd_workspace_size(N, H, abi.DTYPE_F32, ctypes.byref(m)) == 0 and m.value == n.value
+    assert n.value <= 2 * 1024 * 65536 * 4 + 256  # bounded whatever N is
+    assert L.plp_layer_norm_bwd_workspace_size(8, 8, 9, ctypes.byref(n)) == abi.PLP_E_INVALID
+    assert L.plp_layer_norm_bwd_workspace_size(8, 8, 0, None) == abi.PLP_E_INVALID
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    import rl_policy_gradient_amd as plp
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    with pytest.raises(ValueError, match="GPU"):
+        plp.layer_norm_fwd(x, w)
+    with pytest.raises(ValueError, match="GPU"):
+        plp.layer_norm_bwd(x, x, w, torch.ones(4), torch.ones(4))
