@@ -316,8 +316,8 @@ PLP_API int plp_policy_loss_from_logprobs(const plp_args* args, const float* log
 
 /* ---- Operators around the fused loss ---------------------------------------
  * The other calls of a policy's training loop: the final norm that gives
- * `hidden` and takes grad_hidden back. They follow the
- * conventions above, but for alignment: a tensor needs only the alignment of
+ * `hidden` and takes grad_hidden back, and the AdamW step that takes
+ * grad_weight and grad_bias. They follow the conventions above, but for alignment: a tensor needs only the alignment of
  * its elements (16-byte aligned rows take the wide path). These entry points
  * were added to ABI version 5, whose existing calls are unchanged. */
 
@@ -344,6 +344,49 @@ PLP_API int plp_layer_norm_bwd(const void* grad_y, const void* x, const void* we
                                const float* rstd, int64_t N, int32_t H, int32_t dtype, int32_t rms, void* grad_x,
                                void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
                                hipStream_t stream);
+
+/* One tensor of plp_adamw_step. All arrays hold numel elements, in place. */
+typedef struct plp_adamw_tensor {
+  void* param;                  /* [numel] param_dtype */
+  const void* grad;             /* [numel] grad_dtype */
+  float* master;                /* [numel] fp32 copy of a bf16 param, or NULL. Given, the step
+                                   works on it and param becomes its nearest bf16. */
+  void* exp_avg;                /* first moment: [numel] fp32, or u8 e4m3 codes */
+  void* exp_avg_sq;             /* second moment: [numel] fp32, or u8 e4m3 codes of its ROOT */
+  float* exp_avg_scale;         /* state_bits 8: [ceil(numel/256)] fp32, value = code * scale of its */
+  float* exp_avg_sq_scale;      /*   256 consecutive elements; state_bits 32: NULL */
+  int64_t numel;                /* 0 .. 2^35 */
+  int32_t param_dtype, grad_dtype; /* plp_dtype, independent of each other */
+  int32_t state_bits;           /* 32 or 8 */
+  float weight_decay;           /* decoupled: p (1 - lr weight_decay), >= 0 */
+} plp_adamw_tensor;
+
+typedef struct plp_adamw_args {
+  uint32_t struct_size;         /* sizeof(plp_adamw_args) */
+  uint32_t tensor_size;         /* sizeof(plp_adamw_tensor) */
+  double lr, beta1, beta2, eps; /* lr >= 0, betas in [0,1), eps >= 0 */
+  int64_t step;                 /* this step's number, from 1 */
+  const int64_t* step_dev;      /* [1] device: read instead of step (below 1 counts as 1), or NULL */
+  const float* lr_dev;          /* [1] device: read instead of lr, or NULL. Both let a captured
+                                   graph be replayed with new values. */
+  const float* grad_scale;      /* [1] device: factor on every gradient (a clipping coefficient),
+                                   or NULL for 1. Not finite: the whole step changes nothing. */
+} plp_adamw_args;
+
+/* One AdamW step over `count` tensors (host array, read before the call
+ * returns), up to 40 of them a launch:
+ *   g = grad_scale grad, m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * 8-bit states: each block of 256 elements is stored as the nearest e4m3 codes
+ * (four significant bits, largest 448) under the scale max|x| / 448, after the
+ * step has used the unrounded values; a root above zero keeps a code above
+ * zero; an element that is not finite is stored as NaN (0x7f) and leaves its
+ * block's scale alone. All-zero codes and scales are the initial state. Arrays
+ * need the alignment of their elements; the arrays of one tensor must not
+ * overlap (checked), nor those of different tensors (not checked). Errors:
+ * PLP_E_INVALID, PLP_E_HIP. */
+PLP_API int plp_adamw_step(const plp_adamw_args* args, const plp_adamw_tensor* tensors, int32_t count,
+                           hipStream_t stream);
 
 /* ---- Measurement helpers (not part of the method) -------------------------
  * Per-kernel timing of the two LM-head sweeps with HIP events recorded on the

@@ -17,7 +17,7 @@ import torch
 from . import _abi
 from ._abi import METRIC_NAMES, PlpError  # noqa: F401
 from ._marshal import _check_vec, _dtype_code, _ptr, _stream, _workspace
-from .operators import layer_norm_bwd, layer_norm_fwd
+from .operators import AdamWTable, adamw_state, adamw_step, adamw_table, layer_norm_bwd, layer_norm_fwd
 
 __all__ = [
     "fused_lmhead_policy_loss_fwd_bwd",
@@ -30,6 +30,10 @@ __all__ = [
     "workspace_size",
     "layer_norm_fwd",
     "layer_norm_bwd",
+    "adamw_state",
+    "adamw_table",
+    "adamw_step",
+    "AdamWTable",
     "METRIC_NAMES",
     "PlpError",
 ]

@@ -87,6 +87,38 @@ class PlpOutputs(ctypes.Structure):
     ]
 
 
+class PlpAdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("param", _vp),
+        ("grad", _vp),
+        ("master", _vp),
+        ("exp_avg", _vp),
+        ("exp_avg_sq", _vp),
+        ("exp_avg_scale", _vp),
+        ("exp_avg_sq_scale", _vp),
+        ("numel", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32),
+        ("weight_decay", ctypes.c_float),
+    ]
+
+
+class PlpAdamwArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("tensor_size", ctypes.c_uint32),
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("step_dev", _vp),
+        ("lr_dev", _vp),
+        ("grad_scale", _vp),
+    ]
+
+
 class PlpError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"plp error {code}: {msg}")
@@ -94,7 +126,8 @@ class PlpError(RuntimeError):
 
 
 # entry points added to ABI version 5 after its first libraries
-_LATER = ("plp_layer_norm_fwd", "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd")
+_LATER = ("plp_layer_norm_fwd", "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd",
+          "plp_adamw_step")
 
 _lib = None
 
@@ -136,6 +169,7 @@ def lib() -> ctypes.CDLL:
     L.plp_layer_norm_fwd.argtypes = [_vp, _vp, _vp, i64, i32, i32, i32, f64, _vp, _vp, _vp, _vp]
     L.plp_layer_norm_bwd_workspace_size.argtypes = [i64, i32, i32, P(sz)]
     L.plp_layer_norm_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, i64, i32, i32, i32, _vp, _vp, _vp, _vp, sz, _vp]
+    L.plp_adamw_step.argtypes = [P(PlpAdamwArgs), P(PlpAdamwTensor), i32, _vp]
     L.plp_profile_start.argtypes = [ctypes.c_int32]
     L.plp_profile_stop.argtypes = [P(ctypes.c_double), P(ctypes.c_int32)]
     L.plp_profile_stop_n.argtypes = [P(ctypes.c_double), P(ctypes.c_int32), ctypes.c_int32]
@@ -147,7 +181,7 @@ def lib() -> ctypes.CDLL:
                  "plp_selective_entropy_prepared", "plp_entropy_quantile_mask_workspace_size", "plp_entropy_quantile_mask",
                  "plp_entropy_quantile_mask_noalloc", "plp_prepared_weight_size", "plp_prepare_weight",
                  "plp_policy_loss_workspace_size", "plp_policy_loss_from_logprobs", "plp_layer_norm_fwd",
-                 "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd"):
+                 "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd", "plp_adamw_step"):
         getattr(L, name).restype = ctypes.c_int
     if L.plp_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI version {L.plp_abi_version()}, this binding {ABI_VERSION}: "

@@ -24,6 +24,46 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Workgroups of one AdamW launch (times 256 threads stays below 2^32), and the
+// largest tensor, which fits one.
+constexpr int64_t kMaxAdamGrid = (int64_t)1 << 23;
+constexpr int64_t kMaxAdamNumel = kMaxAdamGrid * kAdamTile;
+
+bool in_unit(double b) { return b >= 0.0 && b < 1.0; }
+
+int check_adamw_tensor(const plp_adamw_tensor& t, int i) {
+  if (t.numel < 0 || t.numel > kMaxAdamNumel)
+    return fail(PLP_E_INVALID, "tensor %d: numel=%lld outside [0, 2^35]", i, (long long)t.numel);
+  if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype))
+    return fail(PLP_E_INVALID, "tensor %d: unknown dtype (param %d, grad %d)", i, t.param_dtype, t.grad_dtype);
+  if (t.state_bits != 8 && t.state_bits != 32)
+    return fail(PLP_E_INVALID, "tensor %d: state_bits must be 8 or 32 (got %d)", i, t.state_bits);
+  if (!(t.weight_decay >= 0.f) || !isfinite(t.weight_decay))
+    return fail(PLP_E_INVALID, "tensor %d: weight_decay must be finite and >= 0", i);
+  if (t.master && t.param_dtype != PLP_DTYPE_BF16)
+    return fail(PLP_E_INVALID, "tensor %d: a master copy is for bf16 parameters", i);
+  if (t.numel == 0) return PLP_OK;
+  const bool b8 = t.state_bits == 8;
+  if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq)
+    return fail(PLP_E_INVALID, "tensor %d: param, grad, exp_avg and exp_avg_sq are required", i);
+  if (b8 != (t.exp_avg_scale != nullptr) || b8 != (t.exp_avg_sq_scale != nullptr))
+    return fail(PLP_E_INVALID, "tensor %d: 8-bit states have two arrays of scales, 32-bit states none", i);
+  const size_t n = (size_t)t.numel, pe = esize(t.param_dtype), ge = esize(t.grad_dtype), se = b8 ? 1 : 4;
+  const size_t sb = (n + kAdamBlock - 1) / kAdamBlock * sizeof(float);
+  if (misaligned(t.param, pe) || misaligned(t.grad, ge) || misaligned(t.master, 4) || misaligned(t.exp_avg, se) ||
+      misaligned(t.exp_avg_sq, se) || misaligned(t.exp_avg_scale, 4) || misaligned(t.exp_avg_sq_scale, 4))
+    return fail(PLP_E_INVALID, "tensor %d: an array is not aligned to its elements", i);
+  const struct {
+    const void* p;
+    size_t n;
+  } r[] = {{t.param, n * pe},        {t.master, n * 4},           {t.exp_avg, n * se}, {t.exp_avg_sq, n * se},
+           {t.exp_avg_scale, sb}, {t.exp_avg_sq_scale, sb}, {t.grad, n * ge}};
+  for (int x = 0; x < 7; ++x)
+    for (int y = 0; y < x; ++y)
+      if (overlap(r[x].p, r[x].n, r[y].p, r[y].n)) return fail(PLP_E_INVALID, "tensor %d: two of its arrays overlap", i);
+  return PLP_OK;
+}
+
 constexpr int kMaxNormH = 65536;
 
 int check_norm_sizes(int64_t N, int32_t H, int32_t dtype) {
@@ -96,6 +136,72 @@ PLP_API int plp_layer_norm_bwd(const void* grad_y, const void* x, const void* we
   HIP_TRY(launch_norm_bwd(NormBwd{grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias, (float*)ws, N, H,
                                   dtype, rms ? 1 : 0},
                           st));
+  return ok();
+}
+
+PLP_API int plp_adamw_step(const plp_adamw_args* a, const plp_adamw_tensor* tensors, int32_t count, hipStream_t st) {
+  if (!a) return fail(PLP_E_INVALID, "args is NULL");
+  if (a->struct_size < sizeof(plp_adamw_args) || a->tensor_size != sizeof(plp_adamw_tensor))
+    return fail(PLP_E_INVALID, "args->struct_size %u or tensor_size %u is not this library's (%zu, %zu)",
+                a->struct_size, a->tensor_size, sizeof(plp_adamw_args), sizeof(plp_adamw_tensor));
+  if (count < 0 || (count > 0 && !tensors)) return fail(PLP_E_INVALID, "tensors is NULL or count negative");
+  if (!isfinite(a->lr) || a->lr < 0.0) return fail(PLP_E_INVALID, "lr must be finite and >= 0");
+  if (!in_unit(a->beta1) || !in_unit(a->beta2)) return fail(PLP_E_INVALID, "beta1 and beta2 must lie in [0, 1)");
+  if (!(a->eps >= 0.0) || !isfinite(a->eps)) return fail(PLP_E_INVALID, "eps must be finite and >= 0");
+  if (!a->step_dev && a->step < 1) return fail(PLP_E_INVALID, "step counts from 1 (got %lld)", (long long)a->step);
+  if (misaligned(a->step_dev, 8) || misaligned(a->lr_dev, 4) || misaligned(a->grad_scale, 4))
+    return fail(PLP_E_INVALID, "step_dev, lr_dev or grad_scale is not aligned to its type");
+  for (int i = 0; i < count; ++i) {
+    int rc = check_adamw_tensor(tensors[i], i);
+    if (rc) return rc;
+  }
+  AdamLaunch l;
+  l.b1 = (float)a->beta1;
+  l.c1 = (float)(1.0 - a->beta1);
+  l.b2 = (float)a->beta2;
+  l.c2 = (float)(1.0 - a->beta2);
+  l.eps = (float)a->eps;
+  l.lr = a->lr;
+  l.ln_b1 = log(a->beta1);  // -inf for 0: 1 - b^t is 1
+  l.ln_b2 = log(a->beta2);
+  l.step = a->step;
+  l.step_dev = a->step_dev;
+  l.lr_dev = a->lr_dev;
+  l.grad_scale = a->grad_scale;
+  l.step_size = l.inv_root = 0.f;
+  if (!a->step_dev) {
+    l.step_size = (float)(a->lr / -expm1((double)a->step * l.ln_b1));
+    l.inv_root = (float)(1.0 / sqrt(-expm1((double)a->step * l.ln_b2)));
+  }
+  l.count = 0;
+  l.first[0] = 0;
+  for (int i = 0; i < count; ++i) {
+    const plp_adamw_tensor& t = tensors[i];
+    if (t.numel == 0) continue;
+    const uint32_t groups = (uint32_t)((t.numel + kAdamTile - 1) / kAdamTile);
+    if (l.count == kAdamMaxTensors || l.first[l.count] + groups > kMaxAdamGrid) {
+      HIP_TRY(launch_adamw(l, st));
+      l.count = 0;
+    }
+    AdamTensor& d = l.t[l.count];
+    d.param = t.param;
+    d.grad = t.grad;
+    d.master = t.master;
+    d.m = t.exp_avg;
+    d.v = t.exp_avg_sq;
+    d.ms = t.exp_avg_scale;
+    d.vs = t.exp_avg_sq_scale;
+    d.n = t.numel;
+    d.decay = a->lr_dev ? t.weight_decay : (float)(1.0 - a->lr * (double)t.weight_decay);
+    d.param_bf16 = t.param_dtype == PLP_DTYPE_BF16;
+    d.grad_bf16 = t.grad_dtype == PLP_DTYPE_BF16;
+    d.bits8 = t.state_bits == 8;
+    d.wide = !(misaligned(t.param, 16) || misaligned(t.grad, 16) || misaligned(t.master, 16) ||
+               misaligned(t.exp_avg, 16) || misaligned(t.exp_avg_sq, 16));
+    l.first[l.count + 1] = l.first[l.count] + groups;
+    ++l.count;
+  }
+  if (l.count > 0) HIP_TRY(launch_adamw(l, st));
   return ok();
 }
 

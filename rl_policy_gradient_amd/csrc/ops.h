@@ -35,4 +35,36 @@ hipError_t launch_norm_bwd(const NormBwd& a, hipStream_t st);
 // end; a function of the sizes alone, so results do not depend on the device.
 int norm_bwd_groups(int64_t N, int H);
 
+// One tensor of the AdamW step (a plp_adamw_tensor, checked).
+struct AdamTensor {
+  void* param;
+  const void* grad;
+  float* master;       // or NULL: the step works on param
+  void* m;             // fp32, or e4m3 codes
+  void* v;             // fp32 second moment, or e4m3 codes of its root
+  float *ms, *vs;      // 8-bit states: one scale per kAdamBlock elements
+  int64_t n;
+  float decay;         // 1 - lr weight_decay (weight_decay when the rate is read on the device)
+  uint8_t param_bf16, grad_bf16, bits8, wide;  // wide: every array 16-byte aligned
+};
+constexpr int kAdamBlock = 256;   // elements of one scale
+constexpr int kAdamTile = 4096;   // elements a workgroup takes
+// Tensors of one launch: the table goes by value in the kernel's arguments,
+// which hold 4 KB.
+constexpr int kAdamMaxTensors = 40;
+struct AdamLaunch {
+  AdamTensor t[kAdamMaxTensors];
+  uint32_t first[kAdamMaxTensors + 1];  // the workgroup each tensor begins at
+  int count;
+  float b1, c1, b2, c2;      // beta and 1 - beta
+  float eps;
+  float step_size, inv_root; // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), unless step_dev or lr_dev
+  double lr, ln_b1, ln_b2;
+  const int64_t* step_dev;
+  int64_t step;
+  const float *lr_dev, *grad_scale;
+};
+static_assert(sizeof(AdamLaunch) <= 4096, "kernel arguments");
+hipError_t launch_adamw(const AdamLaunch& a, hipStream_t st);
+
 }  // namespace plp

@@ -1,14 +1,15 @@
 """The operators around the fused loss in a policy's training loop.
 
 ``layer_norm_fwd`` gives the hidden states the fused loss takes and
-``layer_norm_bwd`` takes its grad_hidden back. Like the rest of the package
+``layer_norm_bwd`` takes its grad_hidden back; ``adamw_step`` takes the
+gradients of the weights, over every tensor of the model at once. Like the rest of the package
 these are bindings: the work is done by HIP kernels behind include/plp.h,
 enqueued on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import Optional, Sequence, Union
 
 import torch
 
@@ -91,3 +92,131 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
                                         _ptr(res.get("grad_bias")), ws.data_ptr(), ws.numel() * ws.element_size(),
                                         _stream(dev)))
     return res
+
+
+ADAMW_BLOCK = 256  # elements of one scale of the 8-bit states
+_SCALED = {"exp_avg": "exp_avg_scale", "exp_rms": "exp_rms_scale"}
+
+
+def adamw_state(param: torch.Tensor, *, bits: int = 32, master: bool = False) -> dict:
+    """The state of one parameter before its first step. bits=32: "exp_avg"
+    and "exp_avg_sq" in fp32; bits=8: "exp_avg" and "exp_rms" (the second
+    moment's root) as float8_e4m3fn codes with an fp32 scale per 256 elements
+    in "exp_avg_scale" and "exp_rms_scale". master=True adds an fp32 copy of a
+    bfloat16 parameter, on which the step then works."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+    new = lambda n, dt: torch.zeros(n, dtype=dt, device=param.device)  # noqa: E731
+    if bits == 32:
+        st = {"exp_avg": new(param.shape, torch.float32), "exp_avg_sq": new(param.shape, torch.float32)}
+    else:
+        blocks = -(-param.numel() // ADAMW_BLOCK)
+        st = {k: new(param.shape, torch.uint8).view(torch.float8_e4m3fn) for k in _SCALED}
+        st.update({k: new(blocks, torch.float32) for k in _SCALED.values()})
+    if master:
+        if param.dtype != torch.bfloat16:
+            raise ValueError("a master copy is for bfloat16 parameters")
+        st["master"] = param.detach().float()
+    return st
+
+
+class AdamWTable:
+    """A checked list of tensors for adamw_step, which keeps them alive. Build
+    it again when a tensor is replaced (a gradient newly allocated)."""
+
+    def __init__(self, entries, tensors, device):
+        self.count = len(entries)
+        self.device = device
+        self.tensors = tensors
+        self._array = (_abi.PlpAdamwTensor * max(1, self.count))(*entries)
+
+
+def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[dict], *,
+                weight_decay: Union[float, Sequence[float]] = 0.0) -> AdamWTable:
+    """The tensors of an AdamW step, checked once for all steps: params and
+    grads float32 or bfloat16 in any combination, states as adamw_state makes
+    them (8 and 32 bits may be mixed), weight_decay one value or one per
+    tensor. All are contiguous, on one GPU, and no two overlap but for
+    gradients, which are only read."""
+    params, grads, states = list(params), list(grads), list(states)
+    if not len(params) == len(grads) == len(states):
+        raise ValueError(f"{len(params)} params, {len(grads)} grads and {len(states)} states")
+    decay = [float(weight_decay)] * len(params) if not hasattr(weight_decay, "__len__") else [float(w) for w in
+                                                                                              weight_decay]
+    if len(decay) != len(params):
+        raise ValueError(f"{len(decay)} weight decays for {len(params)} tensors")
+    entries, keep, ranges, dev = [], [], [], None
+    for i, (p, g, st, wd) in enumerate(zip(params, grads, states, decay)):
+        bits = 8 if "exp_rms" in st else 32
+        n = p.numel()
+        names = list(_SCALED) + list(_SCALED.values()) if bits == 8 else ["exp_avg", "exp_avg_sq"]
+        want = {k: (n, torch.float8_e4m3fn if bits == 8 else torch.float32) for k in names}
+        want.update({k: (-(-n // ADAMW_BLOCK), torch.float32) for k in _SCALED.values() if k in want})
+        if st.get("master") is not None:
+            want["master"] = (n, torch.float32)
+        for k, (m, dt) in want.items():
+            if k not in st:
+                raise ValueError(f"states[{i}] has no {k!r}")
+            _check_vec(st[k], m, dt, f"states[{i}][{k!r}]")
+        if g.numel() != n:
+            raise ValueError(f"grads[{i}]: {g.numel()} elements, the parameter has {n}")
+        written = {"params": p, **{k: st[k] for k in want}}
+        d = _one_device(grads=g, **written)
+        if dev is not None and d != dev:
+            raise ValueError(f"tensor {i} is on {d}, the first on {dev}")
+        dev = d
+        e = _abi.PlpAdamwTensor()
+        e.param, e.grad, e.master = _ptr(p), _ptr(g), _ptr(st.get("master"))
+        e.exp_avg, e.exp_avg_sq = _ptr(st["exp_avg"]), _ptr(st["exp_rms" if bits == 8 else "exp_avg_sq"])
+        if bits == 8:
+            e.exp_avg_scale, e.exp_avg_sq_scale = _ptr(st["exp_avg_scale"]), _ptr(st["exp_rms_scale"])
+        e.numel, e.state_bits, e.weight_decay = n, bits, wd
+        e.param_dtype, e.grad_dtype = _dtype_code(p), _dtype_code(g)
+        entries.append(e)
+        keep.append((p, g, st))
+        ranges += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{k} of tensor {i}", True)
+                   for k, t in written.items() if t.numel()]
+        ranges += [(g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), f"grad of tensor {i}", False)] * (n > 0)
+    ranges.sort()
+    end, end_w, who, who_w = 0, 0, "", ""  # the furthest end so far, of all and of what is written
+    for a, b, name, w in ranges:
+        if a < (end if w else end_w):
+            raise ValueError(f"{name} overlaps {who if w else who_w}")
+        if b > end:
+            end, who = b, name
+        if w and b > end_w:
+            end_w, who_w = b, name
+    return AdamWTable(entries, keep, dev)
+
+
+def adamw_step(table: AdamWTable, *, lr: Union[float, torch.Tensor], step: Union[int, torch.Tensor],
+               betas=(0.9, 0.999), eps: float = 1e-8, grad_scale: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step over a table's tensors, in place (plp_adamw_step). step
+    counts from 1. lr (fp32 [1]) and step (int64 [1]) may be device tensors,
+    read when the step runs, so that a captured graph can be replayed.
+    grad_scale (fp32 [1] on the device) multiplies every gradient; where it is
+    not finite the step changes nothing."""
+    a = _abi.PlpAdamwArgs()
+    a.struct_size, a.tensor_size = ctypes.sizeof(a), ctypes.sizeof(_abi.PlpAdamwTensor)
+    a.beta1, a.beta2, a.eps = float(betas[0]), float(betas[1]), float(eps)
+    scalars = {k: t for k, t in (("lr", lr), ("step", step), ("grad_scale", grad_scale)) if
+               isinstance(t, torch.Tensor)}
+    for name, t in scalars.items():
+        _check_vec(t, 1, torch.int64 if name == "step" else torch.float32, name)
+        if table.device is not None and t.device != table.device:
+            raise ValueError(f"{name} is on {t.device}, the tensors on {table.device}")
+    if "lr" in scalars:
+        a.lr_dev = _ptr(lr)
+    else:
+        a.lr = float(lr)
+    if "step" in scalars:
+        a.step_dev = _ptr(step)
+    else:
+        a.step = int(step)
+    a.grad_scale = _ptr(grad_scale)
+    L = _abi.lib()
+    if table.count == 0:
+        _abi.check(L.plp_adamw_step(ctypes.byref(a), table._array, 0, None))
+        return
+    with torch.cuda.device(table.device):
+        _abi.check(L.plp_adamw_step(ctypes.byref(a), table._array, table.count, _stream(table.device)))

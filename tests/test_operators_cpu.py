@@ -99,3 +99,67 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         plp.layer_norm_fwd(x, w)
     with pytest.raises(ValueError, match="GPU"):
         plp.layer_norm_bwd(x, x, w, torch.ones(4), torch.ones(4))
+
+
+def adamw(count=1, tensor=None, **kw):
+    t = (abi.PlpAdamwTensor * 1)()
+    for i, k in enumerate(("param", "grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")):
+        setattr(t[0], k, 0x10000000 * (i + 1))
+    t[0].numel, t[0].state_bits, t[0].weight_decay = 1000, 8, 0.1
+    t[0].param_dtype = t[0].grad_dtype = abi.DTYPE_BF16
+    for k, v in (tensor or {}).items():
+        setattr(t[0], k, v)
+    a = abi.PlpAdamwArgs()
+    a.struct_size, a.tensor_size = ctypes.sizeof(a), ctypes.sizeof(abi.PlpAdamwTensor)
+    a.lr, a.beta1, a.beta2, a.eps, a.step = 1e-3, 0.9, 0.999, 1e-8, 1
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return _lib().plp_adamw_step(ctypes.byref(a), t, count, None)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(struct_size=8), "struct_size"), (dict(tensor_size=72), "tensor_size"), (dict(count=-1), "count"),
+    (dict(lr=-1.0), "lr"), (dict(lr=float("inf")), "lr"), (dict(beta1=1.0), "beta1"), (dict(beta2=-0.1), "beta1"),
+    (dict(beta2=float("nan")), "beta1"), (dict(eps=-1e-8), "eps"), (dict(step=0), "step"),
+    (dict(step_dev=0x1004), "aligned"), (dict(lr_dev=0x1002), "aligned"), (dict(grad_scale=0x1001), "aligned"),
+    (dict(tensor=dict(numel=-1)), "numel"), (dict(tensor=dict(numel=(1 << 35) + 1)), "numel"),
+    (dict(tensor=dict(param_dtype=2)), "dtype"), (dict(tensor=dict(grad_dtype=-1)), "dtype"),
+    (dict(tensor=dict(state_bits=4)), "state_bits"), (dict(tensor=dict(weight_decay=-0.1)), "weight_decay"),
+    (dict(tensor=dict(weight_decay=float("nan"))), "weight_decay"),
+    (dict(tensor=dict(param_dtype=abi.DTYPE_F32)), "master"),
+    (dict(tensor=dict(param=None)), "required"), (dict(tensor=dict(grad=None)), "required"),
+    (dict(tensor=dict(exp_avg=None)), "required"), (dict(tensor=dict(exp_avg_sq=None)), "required"),
+    (dict(tensor=dict(exp_avg_scale=None)), "scales"), (dict(tensor=dict(exp_avg_sq_scale=None)), "scales"),
+    (dict(tensor=dict(state_bits=32)), "scales"), (dict(tensor=dict(param=0x10000001)), "aligned"),
+    (dict(tensor=dict(master=0x30000002)), "aligned"), (dict(tensor=dict(grad=0x10000000)), "overlap"),
+    (dict(tensor=dict(exp_avg_sq=0x40000000 + 999)), "overlap"), (dict(tensor=dict(exp_avg_scale=0x70000008)), "overlap"),
+])
+def test_adamw_refuses(kw, msg):
+    assert adamw(**kw) == abi.PLP_E_INVALID
+    assert msg in _err()
+
+
+def test_adamw_of_nothing():
+    assert adamw(count=0) == abi.PLP_OK
+    assert adamw(tensor=dict(numel=0, param=None, grad=None)) == abi.PLP_OK
+
+
+def test_operator_structs_match_header(tmp_path):
+    """sizeof and every offsetof of the operators' structs against the ctypes mirror."""
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    structs = {"plp_adamw_tensor": abi.PlpAdamwTensor, "plp_adamw_args": abi.PlpAdamwArgs}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "plp.h"', "int main(void){"]
+    for name, cls in structs.items():
+        lines.append(f'printf("{name} . %zu\\n", sizeof({name}));')
+        lines += [f'printf("{name} {f} %zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    c = tmp_path / "probe.c"
+    c.write_text("\n".join(lines + ["return 0;}"]))
+    exe = tmp_path / "probe"
+    r = subprocess.run(["gcc", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(root, "include"), "-I", "/opt/rocm/include",
+                        str(c), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    for ln in subprocess.run([str(exe)], capture_output=True, text=True).stdout.splitlines():
+        name, field, n = ln.split()
+        cls = structs[name]
+        assert int(n) == (ctypes.sizeof(cls) if field == "." else getattr(cls, field).offset), ln
