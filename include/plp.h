@@ -315,9 +315,9 @@ PLP_API int plp_policy_loss_from_logprobs(const plp_args* args, const float* log
                                           hipStream_t stream);
 
 /* ---- Operators around the fused loss ---------------------------------------
- * The other calls of a policy's training loop: the final norm that gives
- * `hidden` and takes grad_hidden back, and the AdamW step that takes
- * grad_weight and grad_bias. They follow the conventions above, but for alignment: a tensor needs only the alignment of
+ * The other calls of a policy's training loop: sampling the completions (the
+ * targets and their old_logp), the final norm that gives `hidden` and takes
+ * grad_hidden back, and the AdamW step that takes grad_weight and grad_bias. They follow the conventions above, but for alignment: a tensor needs only the alignment of
  * its elements (16-byte aligned rows take the wide path). These entry points
  * were added to ABI version 5, whose existing calls are unchanged. */
 
@@ -387,6 +387,46 @@ typedef struct plp_adamw_args {
  * PLP_E_INVALID, PLP_E_HIP. */
 PLP_API int plp_adamw_step(const plp_adamw_args* args, const plp_adamw_tensor* tensors, int32_t count,
                            hipStream_t stream);
+
+/* Inputs and outputs of plp_sample_tokens. */
+typedef struct plp_sample_args {
+  uint32_t struct_size;         /* sizeof(plp_sample_args) */
+  int32_t dtype;                /* plp_dtype of the logits */
+  int64_t N;                    /* rows, >= 0 */
+  int32_t V;                    /* vocabulary size, 1 .. 2^20 */
+  int32_t top_k;                /* 0 (or >= V): no limit */
+  int64_t row_stride;           /* elements from one row to the next, >= 0; a row is contiguous */
+  const void* logits;           /* [N,V]; -inf: the token is masked out */
+  const float* uniforms;        /* [N] in [0,1), one a row */
+  float temperature;            /* >= 0; 0: the largest logit */
+  float top_p;                  /* in [0,1]; 1: no limit */
+  float min_p;                  /* in [0,1]; 0: no limit */
+  int32_t pad0;
+  const float* temperature_rows;/* [N] one a row instead of the value above, or NULL */
+  const int32_t* top_k_rows;    /* [N] or NULL; below 1: no limit */
+  const float* top_p_rows;      /* [N] or NULL; at or above 1: no limit, below 0 as 0 */
+  const float* min_p_rows;      /* [N] or NULL; at or below 0: no limit, above 1 as 1 */
+  int64_t* token_out;           /* [N] */
+  float* logp_out;              /* [N] or NULL: log-prob of the token under softmax(logits / temperature),
+                                   what the losses above take as old_logp */
+  float* kept_logp_out;         /* [N] or NULL: its log-prob among the kept tokens, from which it was drawn */
+} plp_sample_args;
+
+/* One token a row. With w_i = exp((z_i - max z) / temperature) and the tokens
+ * ordered by falling logit, equal ones by index: top_k keeps the first k,
+ * top_p of those the ones before which the mass is below top_p times theirs
+ * (so at least one), min_p those with w_i >= min_p. The token is the first, by
+ * index, at which the running sum of the kept weights exceeds u times their
+ * sum. Weights are formed in 64 bits and added exactly, so a row's result
+ * depends on that row alone. temperature 0 takes the first of the largest
+ * logits and gives both log-probs as 0. A row that has no distribution (a
+ * NaN, +inf, nothing above -inf; a setting or uniform that is NaN, a negative
+ * or infinite temperature) gets token -1 and NaN log-probs. Uniforms outside
+ * [0,1) are taken as the nearest inside. N = 0 does nothing. Errors:
+ * PLP_E_INVALID, PLP_E_UNSUPPORTED (V > 2^20), PLP_E_WORKSPACE, PLP_E_HIP. */
+PLP_API int plp_sample_tokens_workspace_size(int64_t N, int32_t V, size_t* bytes);
+PLP_API int plp_sample_tokens(const plp_sample_args* args, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
 
 /* ---- Measurement helpers (not part of the method) -------------------------
  * Per-kernel timing of the two LM-head sweeps with HIP events recorded on the

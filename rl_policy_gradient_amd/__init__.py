@@ -17,7 +17,8 @@ import torch
 from . import _abi
 from ._abi import METRIC_NAMES, PlpError  # noqa: F401
 from ._marshal import _check_vec, _dtype_code, _ptr, _stream, _workspace
-from .operators import AdamWTable, adamw_state, adamw_step, adamw_table, layer_norm_bwd, layer_norm_fwd
+from .operators import (AdamWTable, adamw_state, adamw_step, adamw_table, layer_norm_bwd, layer_norm_fwd,
+                        sample_tokens)
 
 __all__ = [
     "fused_lmhead_policy_loss_fwd_bwd",
@@ -28,6 +29,7 @@ __all__ = [
     "prepare_weight",
     "prepared_weight_size",
     "workspace_size",
+    "sample_tokens",
     "layer_norm_fwd",
     "layer_norm_bwd",
     "adamw_state",

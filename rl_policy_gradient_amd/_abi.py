@@ -119,6 +119,30 @@ class PlpAdamwArgs(ctypes.Structure):
     ]
 
 
+class PlpSampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_int32),
+        ("N", ctypes.c_int64),
+        ("V", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("row_stride", ctypes.c_int64),
+        ("logits", _vp),
+        ("uniforms", _vp),
+        ("temperature", ctypes.c_float),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
+        ("pad0", ctypes.c_int32),
+        ("temperature_rows", _vp),
+        ("top_k_rows", _vp),
+        ("top_p_rows", _vp),
+        ("min_p_rows", _vp),
+        ("token_out", _vp),
+        ("logp_out", _vp),
+        ("kept_logp_out", _vp),
+    ]
+
+
 class PlpError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"plp error {code}: {msg}")
@@ -127,7 +151,7 @@ class PlpError(RuntimeError):
 
 # entry points added to ABI version 5 after its first libraries
 _LATER = ("plp_layer_norm_fwd", "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd",
-          "plp_adamw_step")
+          "plp_adamw_step", "plp_sample_tokens_workspace_size", "plp_sample_tokens")
 
 _lib = None
 
@@ -170,6 +194,8 @@ def lib() -> ctypes.CDLL:
     L.plp_layer_norm_bwd_workspace_size.argtypes = [i64, i32, i32, P(sz)]
     L.plp_layer_norm_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, i64, i32, i32, i32, _vp, _vp, _vp, _vp, sz, _vp]
     L.plp_adamw_step.argtypes = [P(PlpAdamwArgs), P(PlpAdamwTensor), i32, _vp]
+    L.plp_sample_tokens_workspace_size.argtypes = [i64, i32, P(sz)]
+    L.plp_sample_tokens.argtypes = [P(PlpSampleArgs), _vp, sz, _vp]
     L.plp_profile_start.argtypes = [ctypes.c_int32]
     L.plp_profile_stop.argtypes = [P(ctypes.c_double), P(ctypes.c_int32)]
     L.plp_profile_stop_n.argtypes = [P(ctypes.c_double), P(ctypes.c_int32), ctypes.c_int32]
@@ -181,7 +207,8 @@ def lib() -> ctypes.CDLL:
                  "plp_selective_entropy_prepared", "plp_entropy_quantile_mask_workspace_size", "plp_entropy_quantile_mask",
                  "plp_entropy_quantile_mask_noalloc", "plp_prepared_weight_size", "plp_prepare_weight",
                  "plp_policy_loss_workspace_size", "plp_policy_loss_from_logprobs", "plp_layer_norm_fwd",
-                 "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd", "plp_adamw_step"):
+                 "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd", "plp_adamw_step", "plp_sample_tokens_workspace_size",
+                 "plp_sample_tokens"):
         getattr(L, name).restype = ctypes.c_int
     if L.plp_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI version {L.plp_abi_version()}, this binding {ABI_VERSION}: "

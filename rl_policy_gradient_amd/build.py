@@ -16,7 +16,7 @@ OUT = os.path.join(PKG, "libplp.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["lmhead_fwd.hip", "lmhead_fwd_o.hip", "lmhead_mfma.hip", "lmhead_generic.hip", "loss_stage.hip",
-           "plp_api.cpp", "layer_norm.hip", "adamw.hip", "operators_api.cpp"]
+           "plp_api.cpp", "layer_norm.hip", "adamw.hip", "sampling.hip", "operators_api.cpp"]
 
 # Per-source compiler options. Both two-role sweeps are faster without the
 # scheduler's unclustered high-register-pressure rescheduling stage (measured

@@ -66,6 +66,13 @@ int check_adamw_tensor(const plp_adamw_tensor& t, int i) {
 
 constexpr int kMaxNormH = 65536;
 
+size_t carve_sample(void* ws, int64_t N, int32_t V, SampleArgs& a) {
+  Carver c(ws);
+  a.block_sum = c.take<double>((size_t)N * sample_blocks(V));
+  a.block_max = c.take<float>((size_t)N * sample_blocks(V));
+  return c.off;
+}
+
 int check_norm_sizes(int64_t N, int32_t H, int32_t dtype) {
   if (!known_dtype(dtype)) return fail(PLP_E_INVALID, "unknown dtype %d", dtype);
   if (N < 0 || N >= kMaxRows) return fail(PLP_E_INVALID, "N=%lld outside [0, 2^31)", (long long)N);
@@ -202,6 +209,66 @@ PLP_API int plp_adamw_step(const plp_adamw_args* a, const plp_adamw_tensor* tens
     ++l.count;
   }
   if (l.count > 0) HIP_TRY(launch_adamw(l, st));
+  return ok();
+}
+
+PLP_API int plp_sample_tokens_workspace_size(int64_t N, int32_t V, size_t* bytes) {
+  if (!bytes) return fail(PLP_E_INVALID, "bytes is NULL");
+  if (N < 0 || N >= kMaxRows) return fail(PLP_E_INVALID, "N=%lld outside [0, 2^31)", (long long)N);
+  if (V < 1) return fail(PLP_E_INVALID, "V must be >= 1 (got %d)", V);
+  if (V > kSampleMaxV) return fail(PLP_E_UNSUPPORTED, "V=%d is above %d", V, kSampleMaxV);
+  SampleArgs s;
+  *bytes = carve_sample(nullptr, N, V, s);
+  return ok();
+}
+
+PLP_API int plp_sample_tokens(const plp_sample_args* a, void* ws, size_t ws_bytes, hipStream_t st) {
+  if (!a) return fail(PLP_E_INVALID, "args is NULL");
+  if (a->struct_size < sizeof(plp_sample_args))
+    return fail(PLP_E_INVALID, "args->struct_size %u < %zu", a->struct_size, sizeof(plp_sample_args));
+  if (!known_dtype(a->dtype)) return fail(PLP_E_INVALID, "unknown dtype %d", a->dtype);
+  size_t need = 0;
+  int rc = plp_sample_tokens_workspace_size(a->N, a->V, &need);
+  if (rc) return rc;
+  if (a->row_stride < 0) return fail(PLP_E_INVALID, "row_stride must be >= 0");
+  if (!a->temperature_rows && (!(a->temperature >= 0.f) || !isfinite(a->temperature)))
+    return fail(PLP_E_INVALID, "temperature must be finite and >= 0");
+  if (!a->top_k_rows && a->top_k < 0) return fail(PLP_E_INVALID, "top_k must be >= 0");
+  if (!a->top_p_rows && !(a->top_p >= 0.f && a->top_p <= 1.f))
+    return fail(PLP_E_INVALID, "top_p must lie in [0, 1]");
+  if (!a->min_p_rows && !(a->min_p >= 0.f && a->min_p <= 1.f))
+    return fail(PLP_E_INVALID, "min_p must lie in [0, 1]");
+  if (a->N == 0) return ok();
+  if (!a->logits || !a->uniforms || !a->token_out)
+    return fail(PLP_E_INVALID, "logits, uniforms and token_out are required");
+  const void* f32[] = {a->uniforms,   a->temperature_rows, a->top_k_rows,   a->top_p_rows,
+                       a->min_p_rows, a->logp_out,         a->kept_logp_out};
+  for (const void* p : f32)
+    if (misaligned(p, 4)) return fail(PLP_E_INVALID, "an array is not aligned to its elements");
+  if (misaligned(a->logits, esize(a->dtype)) || misaligned(a->token_out, 8))
+    return fail(PLP_E_INVALID, "an array is not aligned to its elements");
+  rc = check_ws(ws, ws_bytes, need);
+  if (rc) return rc;
+  SampleArgs s;
+  carve_sample(ws, a->N, a->V, s);
+  s.logits = a->logits;
+  s.uniforms = a->uniforms;
+  s.tau = a->temperature;
+  s.top_p = a->top_p;
+  s.min_p = a->min_p;
+  s.top_k = a->top_k;
+  s.tau_rows = a->temperature_rows;
+  s.top_p_rows = a->top_p_rows;
+  s.min_p_rows = a->min_p_rows;
+  s.top_k_rows = a->top_k_rows;
+  s.token = a->token_out;
+  s.logp = a->logp_out;
+  s.kept_logp = a->kept_logp_out;
+  s.N = a->N;
+  s.stride = a->row_stride;
+  s.V = a->V;
+  s.dtype = a->dtype;
+  HIP_TRY(launch_sample(s, st));
   return ok();
 }
 

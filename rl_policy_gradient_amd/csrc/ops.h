@@ -67,4 +67,27 @@ struct AdamLaunch {
 static_assert(sizeof(AdamLaunch) <= 4096, "kernel arguments");
 hipError_t launch_adamw(const AdamLaunch& a, hipStream_t st);
 
+// Sampling one token a row of logits; block_max and block_sum are workspace,
+// sample_blocks(V) of each a row.
+struct SampleArgs {
+  const void* logits;
+  const float* uniforms;
+  float tau, top_p, min_p;
+  int top_k;
+  const float *tau_rows, *top_p_rows, *min_p_rows;  // instead of the scalars, or NULL
+  const int32_t* top_k_rows;
+  int64_t* token;
+  float *logp, *kept_logp;
+  double* block_sum;
+  float* block_max;
+  int64_t N, stride;
+  int V, dtype;
+};
+constexpr int kSampleBlock = 256;  // logits of one block
+// Blocks of a row of V logits, the first of which may begin up to seven
+// elements before the row (at a multiple of 16 bytes).
+inline int sample_blocks(int V) { return (V + 7 + kSampleBlock - 1) / kSampleBlock; }
+constexpr int kSampleMaxV = 1 << 20;
+hipError_t launch_sample(const SampleArgs& a, hipStream_t st);
+
 }  // namespace plp

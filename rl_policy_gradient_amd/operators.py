@@ -1,6 +1,7 @@
 """The operators around the fused loss in a policy's training loop.
 
-``layer_norm_fwd`` gives the hidden states the fused loss takes and
+``sample_tokens`` draws the completions, with the log-probs the loss takes as
+old_logp; ``layer_norm_fwd`` gives the hidden states the fused loss takes and
 ``layer_norm_bwd`` takes its grad_hidden back; ``adamw_step`` takes the
 gradients of the weights, over every tensor of the model at once. Like the rest of the package
 these are bindings: the work is done by HIP kernels behind include/plp.h,
@@ -26,6 +27,61 @@ def _out(out: Optional[dict], name: str, shape, dtype, dev) -> torch.Tensor:
         raise ValueError(f"out[{name!r}]: expected {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
     return t
+
+
+def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: Union[float, torch.Tensor] = 1.0,
+                  top_k: Union[int, torch.Tensor] = 0, top_p: Union[float, torch.Tensor] = 1.0,
+                  min_p: Union[float, torch.Tensor] = 0.0, workspace: Optional[torch.Tensor] = None,
+                  out: Optional[dict] = None) -> dict:
+    """One token a row of logits [N, V] (float32 or bfloat16; rows contiguous,
+    any distance apart) from uniforms fp32 [N] in [0, 1) (plp_sample_tokens).
+    temperature, top_p, min_p (fp32) and top_k (int32) are one value or a
+    device tensor [N]; 0 temperature is greedy, top_k 0, top_p 1 and min_p 0
+    do not limit. Returns {"token": int64 [N], "logp": fp32 [N] under the
+    whole tempered distribution, "kept_logp": fp32 [N] among the kept
+    tokens}, written into out's tensors where it has them; token -1 and NaN
+    for a row without a distribution."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected [N, V], got {tuple(logits.shape)}")
+    N, V = (int(n) for n in logits.shape)
+    rows = {k: t for k, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)) if
+            isinstance(t, torch.Tensor)}
+    dev = _one_device(logits=logits, uniforms=uniforms, **rows)
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("plp needs each row of logits contiguous")
+    _check_vec(uniforms, N, torch.float32, "uniforms")
+    for k, t in rows.items():
+        _check_vec(t, N, torch.int32 if k == "top_k" else torch.float32, k)
+    a = _abi.PlpSampleArgs()
+    a.struct_size, a.dtype = ctypes.sizeof(a), _dtype_code(logits)
+    a.N, a.V, a.row_stride = N, V, int(logits.stride(0)) if N > 1 else V
+    a.logits, a.uniforms = logits.data_ptr(), _ptr(uniforms)
+    if "temperature" in rows:
+        a.temperature_rows = _ptr(temperature)
+    else:
+        a.temperature = float(temperature)
+    if "top_k" in rows:
+        a.top_k_rows = _ptr(top_k)
+    else:
+        a.top_k = int(top_k)
+    if "top_p" in rows:
+        a.top_p_rows = _ptr(top_p)
+    else:
+        a.top_p = float(top_p)
+    if "min_p" in rows:
+        a.min_p_rows = _ptr(min_p)
+    else:
+        a.min_p = float(min_p)
+    L = _abi.lib()
+    n = ctypes.c_size_t()
+    _abi.check(L.plp_sample_tokens_workspace_size(N, V, ctypes.byref(n)))
+    with torch.cuda.device(dev):
+        res = {"token": _out(out, "token", (N,), torch.int64, dev), "logp": _out(out, "logp", (N,), torch.float32, dev),
+               "kept_logp": _out(out, "kept_logp", (N,), torch.float32, dev)}
+        a.token_out, a.logp_out, a.kept_logp_out = _ptr(res["token"]), _ptr(res["logp"]), _ptr(res["kept_logp"])
+        ws = _workspace(n.value, dev, workspace)
+        _abi.check(L.plp_sample_tokens(ctypes.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev)))
+    return res
 
 
 def _norm_sizes(x, weight, bias):

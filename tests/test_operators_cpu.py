@@ -148,7 +148,8 @@ def test_operator_structs_match_header(tmp_path):
     """sizeof and every offsetof of the operators' structs against the ctypes mirror."""
     import subprocess
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    structs = {"plp_adamw_tensor": abi.PlpAdamwTensor, "plp_adamw_args": abi.PlpAdamwArgs}
+    structs = {"plp_adamw_tensor": abi.PlpAdamwTensor, "plp_adamw_args": abi.PlpAdamwArgs,
+               "plp_sample_args": abi.PlpSampleArgs}
     lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "plp.h"', "int main(void){"]
     for name, cls in structs.items():
         lines.append(f'printf("{name} . %zu\\n", sizeof({name}));')
@@ -163,3 +164,54 @@ def test_operator_structs_match_header(tmp_path):
         name, field, n = ln.split()
         cls = structs[name]
         assert int(n) == (ctypes.sizeof(cls) if field == "." else getattr(cls, field).offset), ln
+
+
+def sample(ws=WS, ws_bytes=1 << 24, **kw):
+    a = abi.PlpSampleArgs()
+    a.struct_size, a.dtype = ctypes.sizeof(a), abi.DTYPE_BF16
+    a.N, a.V, a.row_stride = 4, 1000, 1000
+    a.logits, a.uniforms, a.token_out = X, W, Y
+    a.temperature, a.top_p = 1.0, 1.0
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return _lib().plp_sample_tokens(ctypes.byref(a), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(struct_size=8), abi.PLP_E_INVALID, "struct_size"),
+    (dict(dtype=2), abi.PLP_E_INVALID, "dtype"),
+    (dict(N=-1), abi.PLP_E_INVALID, "N="),
+    (dict(N=1 << 31), abi.PLP_E_INVALID, "N="),
+    (dict(V=0), abi.PLP_E_INVALID, "V must"),
+    (dict(V=(1 << 20) + 1), abi.PLP_E_UNSUPPORTED, "V="),
+    (dict(row_stride=-1), abi.PLP_E_INVALID, "row_stride"),
+    (dict(temperature=-0.5), abi.PLP_E_INVALID, "temperature"),
+    (dict(temperature=float("nan")), abi.PLP_E_INVALID, "temperature"),
+    (dict(temperature=float("inf")), abi.PLP_E_INVALID, "temperature"),
+    (dict(top_k=-1), abi.PLP_E_INVALID, "top_k"),
+    (dict(top_p=1.5), abi.PLP_E_INVALID, "top_p"),
+    (dict(top_p=float("nan")), abi.PLP_E_INVALID, "top_p"),
+    (dict(min_p=-0.1), abi.PLP_E_INVALID, "min_p"),
+    (dict(logits=None), abi.PLP_E_INVALID, "required"),
+    (dict(uniforms=None), abi.PLP_E_INVALID, "required"),
+    (dict(token_out=None), abi.PLP_E_INVALID, "required"),
+    (dict(logits=X + 1), abi.PLP_E_INVALID, "aligned"),
+    (dict(token_out=Y + 4), abi.PLP_E_INVALID, "aligned"),
+    (dict(logp_out=M + 2), abi.PLP_E_INVALID, "aligned"),
+    (dict(ws_bytes=64), abi.PLP_E_WORKSPACE, "too small"),
+    (dict(ws=None), abi.PLP_E_WORKSPACE, "NULL"),
+    (dict(ws=WS + 8), abi.PLP_E_WORKSPACE, "aligned"),
+])
+def test_sampling_refuses(kw, code, msg):
+    assert sample(**kw) == code
+    assert msg in _err()
+
+
+def test_sampling_of_nothing_and_workspace():
+    assert sample(N=0, logits=None, uniforms=None, token_out=None, ws=None, ws_bytes=0) == abi.PLP_OK
+    L, n = _lib(), ctypes.c_size_t()
+    for N, V in ((1, 1), (512, 151936), ((1 << 31) - 1, 1 << 20)):
+        assert L.plp_sample_tokens_workspace_size(N, V, ctypes.byref(n)) == 0
+        # a maximum and a sum for each 256 logits, never a copy of them
+        assert N * ((V + 255) // 256) * 12 <= n.value <= N * ((V + 262) // 256) * 12 + 512
+    assert L.plp_sample_tokens_workspace_size(1, 1, None) == abi.PLP_E_INVALID
