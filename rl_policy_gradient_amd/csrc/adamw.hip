@@ -20,17 +20,15 @@ namespace plp {
 
 namespace {
 
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int NT = 256;
 constexpr float kCodeMax = 448.f;      // largest e4m3 value
 constexpr float kCodeMin = 0x1p-9f;    // smallest above zero
 constexpr float kScaleMin = 0x1p-126f; // a smaller scale's inverse would overflow
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
-
-__device__ __forceinline__ float from_e4m3(uint8_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
-__device__ __forceinline__ uint8_t to_e4m3(float x) {
-  return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(x, 0.f, 0, false) & 0xff);
-}
 
 // The scalars of one step.
 struct Scalars {
@@ -69,33 +67,206 @@ __device__ __forceinline__ Updated update(float p, float g, float m, float v, fl
   return u;
 }
 
-__device__ __forceinline__ float load(const void* p, int64_t i, bool bf16) {
-  return bf16 ? (float)((const __bf16*)p)[i] : ((const float*)p)[i];
-}
-
-// Largest finite magnitude over the block of 256 threads.
-__device__ float block_absmax(float x, float* red) {
-  x = finite(x) ? fabsf(x) : 0.f;
+// Four consecutive elements i .. i+3 of an array of n, those at or past n as
+// 0. `wide`: the array is 16-byte aligned (i is a multiple of 4).
+__device__ __forceinline__ f32x4 load4(const float* p, int64_t i, int64_t n, bool wide) {
+  if (wide && i + 4 <= n) return *reinterpret_cast<const f32x4*>(p + i);
+  f32x4 x;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-  __syncthreads();
-  const float r = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  __syncthreads();
-  return r;
+  for (int k = 0; k < 4; ++k) x[k] = i + k < n ? p[i + k] : 0.f;
+  return x;
+}
+__device__ __forceinline__ f32x4 load4(const __bf16* p, int64_t i, int64_t n, bool wide) {
+  if (wide && i + 4 <= n) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p + i);
+    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                 __uint_as_float(u.y & 0xffff0000u)};
+  }
+  f32x4 x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = i + k < n ? (float)p[i + k] : 0.f;
+  return x;
+}
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n, bool wide) {
+  if (wide && i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
+  uint32_t x = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x |= i + k < n ? (uint32_t)p[i + k] << 8 * k : 0u;
+  return x;
+}
+__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, bool wide, f32x4 x) {
+  if (wide && i + 4 <= n) {
+    *reinterpret_cast<f32x4*>(p + i) = x;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + k < n) p[i + k] = x[k];
+}
+__device__ __forceinline__ void store4(__bf16* p, int64_t i, int64_t n, bool wide, f32x4 x) {
+  bf16x4 y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) y[k] = (__bf16)x[k];
+  if (wide && i + 4 <= n) {
+    *reinterpret_cast<bf16x4*>(p + i) = y;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + k < n) p[i + k] = y[k];
+}
+__device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, bool wide, uint32_t x) {
+  if (wide && i + 4 <= n) {
+    *reinterpret_cast<uint32_t*>(p + i) = x;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + k < n) p[i + k] = (uint8_t)(x >> 8 * k);
 }
 
-__device__ __forceinline__ uint8_t encode(float x, float scale, bool positive) {
-  if (!finite(x)) return 0x7f;  // NaN, in its own place only
-  float y = scale > 0.f ? x / scale : 0.f;
-  y = fminf(fmaxf(y, -kCodeMax), kCodeMax);
-  if (positive && x > 0.f && scale > 0.f) y = fmaxf(y, kCodeMin);
-  return to_e4m3(y);
+__device__ __forceinline__ f32x4 from_e4m3(uint32_t c) {
+  return f32x4{__builtin_amdgcn_cvt_f32_fp8(c, 0), __builtin_amdgcn_cvt_f32_fp8(c, 1),
+               __builtin_amdgcn_cvt_f32_fp8(c, 2), __builtin_amdgcn_cvt_f32_fp8(c, 3)};
 }
 
-__device__ __forceinline__ float scale_of(float absmax) {
-  const float s = absmax / kCodeMax;
-  return s < kScaleMin ? 0.f : s;
+// Largest of 64 lanes' values, none negative, in every lane: within quads,
+// half rows and rows of 16 by lane permutations, then across the rows.
+__device__ __forceinline__ float wave_max(float v) {
+#define PLP_DPP_MAX(ctrl, rows) \
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false)))
+  PLP_DPP_MAX(0xb1, 0xf);   // lanes 1 0 3 2 of each quad
+  PLP_DPP_MAX(0x4e, 0xf);   // lanes 2 3 0 1
+  PLP_DPP_MAX(0x141, 0xf);  // mirrored in each half row
+  PLP_DPP_MAX(0x140, 0xf);  // mirrored in each row
+  PLP_DPP_MAX(0x142, 0xa);  // the row before into rows 1 and 3
+  PLP_DPP_MAX(0x143, 0xc);  // row 1 into rows 2 and 3
+#undef PLP_DPP_MAX
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ float finite_max(f32x4 x) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m = fmaxf(m, finite(x[k]) ? fabsf(x[k]) : 0.f);
+  return m;
+}
+
+// The block's scale and its reciprocal (both 0 for a block whose largest value
+// is too small for a scale).
+struct Scale {
+  float s, inv;
+  // x / s, correctly rounded: the reciprocal is, so one residual step makes
+  // the quotient so too (Markstein 1990). Three operations instead of a
+  // division's eleven, and the same code for a value at a tie however the
+  // quotient is formed.
+  __device__ __forceinline__ float divide(float x) const {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, s, x), inv, q);
+  }
+};
+__device__ __forceinline__ Scale scale_of(float absmax) {
+  const float s = absmax * (1.f / kCodeMax);
+  return s < kScaleMin ? Scale{0.f, 0.f} : Scale{s, 1.f / s};
+}
+
+// Four codes. The nearest e4m3 values (ties to even, as the hardware rounds);
+// what is not finite becomes NaN in its own place only.
+__device__ __forceinline__ uint32_t encode(f32x4 x, Scale sc, bool positive) {
+  f32x4 y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    y[k] = fminf(fmaxf(sc.divide(x[k]), -kCodeMax), kCodeMax);
+    if (positive && x[k] > 0.f && sc.inv > 0.f) y[k] = fmaxf(y[k], kCodeMin);
+  }
+  int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  c = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (!finite(x[k])) c = (c & ~(0xff << 8 * k)) | (0x7f << 8 * k);
+  return (uint32_t)c;
+}
+
+// One wave's share of a tile: kRounds blocks of 256 elements, four a lane,
+// 1024 elements apart. All loads are issued before the first use: an HBM-bound
+// pass needs the bytes in flight.
+constexpr int kRounds = kAdamTile / (4 * NT);
+static_assert(kAdamBlock == 4 * 64, "one block of a scale is a wave's four elements a lane");
+
+template <typename P, typename G, bool MASTER, bool BITS8>
+__device__ __forceinline__ void tile(const AdamTensor& t, const Scalars& s, float keep, int64_t begin) {
+  const int64_t n = t.n;
+  const bool wide = t.wide;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  f32x4 p[kRounds], g[kRounds], m[kRounds], v[kRounds];
+  uint32_t mc[kRounds], vc[kRounds];
+  float ms[kRounds], vs[kRounds];
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) {
+    const int64_t i = begin + u * (4 * NT) + wave * kAdamBlock + lane * 4;
+    if (MASTER)
+      p[u] = load4((const float*)t.master, i, n, wide);
+    else
+      p[u] = load4((const P*)t.param, i, n, wide);
+    g[u] = load4((const G*)t.grad, i, n, wide);
+    if (BITS8) {
+      const int64_t b = i / kAdamBlock;
+      mc[u] = load4((const uint8_t*)t.m, i, n, wide);
+      vc[u] = load4((const uint8_t*)t.v, i, n, wide);
+      ms[u] = i < n ? t.ms[b] : 0.f;
+      vs[u] = i < n ? t.vs[b] : 0.f;
+    } else {
+      m[u] = load4((const float*)t.m, i, n, wide);
+      v[u] = load4((const float*)t.v, i, n, wide);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) {
+    const int64_t i = begin + u * (4 * NT) + wave * kAdamBlock + lane * 4;
+    if (BITS8) {
+      const f32x4 r = from_e4m3(vc[u]) * vs[u];
+      m[u] = from_e4m3(mc[u]) * ms[u];
+      v[u] = r * r;
+    }
+    f32x4 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const Updated x = update(p[u][k], g[u][k], m[u][k], v[u][k], keep, s);
+      p[u][k] = x.p;
+      m[u][k] = x.m;
+      v[u][k] = x.v;
+      r[k] = x.r;
+    }
+    if (MASTER) store4(t.master, i, n, wide, p[u]);
+    store4((P*)t.param, i, n, wide, p[u]);
+    if (BITS8) {  // elements past the end are all zero and do not count
+      const Scale sm = scale_of(wave_max(finite_max(m[u]))), sr = scale_of(wave_max(finite_max(r)));
+      store4((uint8_t*)t.m, i, n, wide, encode(m[u], sm, false));
+      store4((uint8_t*)t.v, i, n, wide, encode(r, sr, true));
+      if (lane == 0 && i < n) {
+        t.ms[i / kAdamBlock] = sm.s;
+        t.vs[i / kAdamBlock] = sr.s;
+      }
+    } else {
+      store4((float*)t.m, i, n, wide, m[u]);
+      store4((float*)t.v, i, n, wide, v[u]);
+    }
+  }
+}
+
+template <typename P, bool MASTER>
+__device__ __forceinline__ void tile(const AdamTensor& t, const Scalars& s, float keep, int64_t begin) {
+  if (t.grad_bf16) {
+    if (t.bits8)
+      tile<P, __bf16, MASTER, true>(t, s, keep, begin);
+    else
+      tile<P, __bf16, MASTER, false>(t, s, keep, begin);
+  } else {
+    if (t.bits8)
+      tile<P, float, MASTER, true>(t, s, keep, begin);
+    else
+      tile<P, float, MASTER, false>(t, s, keep, begin);
+  }
 }
 
 // The tensor of this workgroup: one comparison a lane (the table holds fewer
@@ -107,54 +278,24 @@ __device__ __forceinline__ int tensor_of(const AdamLaunch& a) {
   return __builtin_amdgcn_readfirstlane(__popcll(__ballot(after)));
 }
 
-__global__ __launch_bounds__(NT) void adamw_kernel(AdamLaunch a) {
-  __shared__ float red[NT / 64];
+__global__ __launch_bounds__(NT) void adamw_kernel(AdamLaunch) {
+  // the arguments where they lie, in constant memory: an index that varies by
+  // workgroup into a by-value argument makes the compiler copy all of it to
+  // scratch memory first (measured: the step eight times slower)
+  const AdamLaunch& a = *(const AdamLaunch*)(const __attribute__((address_space(4))) AdamLaunch*)
+                            __builtin_amdgcn_kernarg_segment_ptr();
   const int k = tensor_of(a);
   const AdamTensor t = a.t[k];
   const Scalars s = scalars(a);
   if (!finite(s.gscale)) return;  // the whole step is left out
   const float keep = a.lr_dev ? 1.f - s.lr * t.decay : t.decay;
   const int64_t begin = (int64_t)(blockIdx.x - a.first[k]) * kAdamTile;
-  for (int64_t i0 = begin; i0 < begin + kAdamTile && i0 < t.n; i0 += NT) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool in = i < t.n;
-    Updated u{0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      const float p = t.master ? t.master[i] : load(t.param, i, t.param_bf16);
-      const float g = load(t.grad, i, t.grad_bf16);
-      float m, v;
-      if (t.bits8) {
-        const int64_t b = i / kAdamBlock;
-        const float r = from_e4m3(((const uint8_t*)t.v)[i]) * t.vs[b];
-        m = from_e4m3(((const uint8_t*)t.m)[i]) * t.ms[b];
-        v = r * r;
-      } else {
-        m = ((const float*)t.m)[i];
-        v = ((const float*)t.v)[i];
-      }
-      u = update(p, g, m, v, keep, s);
-      if (t.master) t.master[i] = u.p;
-      if (t.param_bf16)
-        ((__bf16*)t.param)[i] = (__bf16)u.p;
-      else
-        ((float*)t.param)[i] = u.p;
-      if (!t.bits8) {
-        ((float*)t.m)[i] = u.m;
-        ((float*)t.v)[i] = u.v;
-      }
-    }
-    if (t.bits8) {  // uniform: one block of 256 elements
-      const float sm = scale_of(block_absmax(u.m, red)), sr = scale_of(block_absmax(u.r, red));
-      if (in) {
-        ((uint8_t*)t.m)[i] = encode(u.m, sm, false);
-        ((uint8_t*)t.v)[i] = encode(u.r, sr, true);
-      }
-      if (threadIdx.x == 0) {
-        t.ms[i0 / kAdamBlock] = sm;
-        t.vs[i0 / kAdamBlock] = sr;
-      }
-    }
-  }
+  if (!t.param_bf16)
+    tile<float, false>(t, s, keep, begin);
+  else if (t.master)
+    tile<__bf16, true>(t, s, keep, begin);
+  else
+    tile<__bf16, false>(t, s, keep, begin);
 }
 
 }  // namespace
