@@ -355,7 +355,7 @@ typedef struct plp_adamw_tensor {
   void* exp_avg_sq;             /* second moment: [numel] fp32, or u8 e4m3 codes of its ROOT */
   float* exp_avg_scale;         /* state_bits 8: [ceil(numel/256)] fp32, value = code * scale of its */
   float* exp_avg_sq_scale;      /*   256 consecutive elements; state_bits 32: NULL */
-  int64_t numel;                /* 0 .. 2^35 */
+  int64_t numel;                /* 0 .. 2^33 */
   int32_t param_dtype, grad_dtype; /* plp_dtype, independent of each other */
   int32_t state_bits;           /* 32 or 8 */
   float weight_decay;           /* decoupled: p (1 - lr weight_decay), >= 0 */
@@ -374,7 +374,7 @@ typedef struct plp_adamw_args {
 } plp_adamw_args;
 
 /* One AdamW step over `count` tensors (host array, read before the call
- * returns), up to 40 of them a launch:
+ * returns), up to 52 of them a launch:
  *   g = grad_scale grad, m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps).
  * 8-bit states: each block of 256 elements is stored as the nearest e4m3 codes

@@ -12,6 +12,7 @@
 #include "ops.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace plp {
 
@@ -35,7 +36,189 @@ __device__ float block_sum(float v, float* red) {
   return r;
 }
 
-// Any H and alignment: one workgroup a row, the row read again for each pass.
+// ---------------------------------------------------------------------------
+// Rows of up to 16384: the row stays in registers, 16 elements a lane, and
+// LPR = 8 .. 1024 lanes (the least power of two that holds it) share a row, so
+// a workgroup of 256 takes 256 / LPR rows at a time and short rows leave no
+// lane idle. V elements are loaded at once: 16 bytes where every array is
+// aligned and H a multiple of that, else one.
+// ---------------------------------------------------------------------------
+constexpr int kPerLane = 16;
+constexpr int kMaxLanes = 1024;
+
+// Sum over the LPR lanes of a row (aligned groups of lanes), in every one of
+// them, in a fixed order: lane permutations up to 16 lanes, exchanges up to a
+// wave, then the waves' sums through LDS (`red`: a float per wave; all threads
+// of the workgroup call).
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#define PLP_DPP_ADD(ctrl) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, false))
+  PLP_DPP_ADD(0xb1);   // lanes 1 0 3 2 of each quad
+  PLP_DPP_ADD(0x4e);   // lanes 2 3 0 1
+  PLP_DPP_ADD(0x141);  // mirrored in each half row of 16
+  if constexpr (LPR >= 16) PLP_DPP_ADD(0x140);  // mirrored in each row
+#undef PLP_DPP_ADD
+  if constexpr (LPR >= 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (LPR >= 64) v += __shfl_xor(v, 32, 64);
+  if constexpr (LPR > 64) {
+    constexpr int W = LPR / 64;
+    const int wave = threadIdx.x >> 6, first = wave / W * W;
+    __syncthreads();  // the sums before this have been read
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += red[first + w];
+  }
+  return v;
+}
+
+// The 16 elements of a lane: V consecutive ones, then V more LPR V further on.
+// Those at or past H are 0.
+template <typename T, int V, int LPR>
+__device__ __forceinline__ void load_row(const T* p, int lane, int H, float (&x)[kPerLane]) {
+  typedef T TV __attribute__((ext_vector_type(V)));
+#pragma unroll
+  for (int c = 0; c < kPerLane / V; ++c) {
+    const int d = (c * LPR + lane) * V;
+    if (d < H) {
+      if constexpr (V == 1) {
+        x[c] = (float)p[d];
+      } else {
+        const TV t = *reinterpret_cast<const TV*>(p + d);
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[c * V + k] = (float)t[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[c * V + k] = 0.f;
+    }
+  }
+}
+
+template <typename T, int V, int LPR>
+__device__ __forceinline__ void store_row(T* p, int lane, int H, const float (&x)[kPerLane]) {
+  typedef T TV __attribute__((ext_vector_type(V)));
+#pragma unroll
+  for (int c = 0; c < kPerLane / V; ++c) {
+    const int d = (c * LPR + lane) * V;
+    if (d < H) {
+      if constexpr (V == 1) {
+        p[d] = (T)x[c];
+      } else {
+        TV t;
+#pragma unroll
+        for (int k = 0; k < V; ++k) t[k] = (T)x[c * V + k];
+        *reinterpret_cast<TV*>(p + d) = t;
+      }
+    }
+  }
+}
+
+// Whether element e of the lane's 16 lies in the row.
+template <int V, int LPR>
+__device__ __forceinline__ bool inside(int e, int lane, int H) {
+  return (e / V * LPR + lane) * V + e % V < H;
+}
+
+template <int LPR>
+constexpr int threads_of = LPR > NT ? LPR : NT;
+
+template <typename T, int V, int LPR>
+__global__ __launch_bounds__(threads_of<LPR>) void norm_fwd_kernel(NormFwd a) {
+  constexpr int slots = threads_of<LPR> / LPR;
+  __shared__ float red[threads_of<LPR> / 64];
+  const int H = a.H, lane = threadIdx.x % LPR;
+  const float inv = 1.f / (float)H;
+  const int64_t row = (int64_t)blockIdx.x * slots + threadIdx.x / LPR;
+  const bool in = row < a.N;
+  float x[kPerLane], w[kPerLane], b[kPerLane];
+  load_row<T, V, LPR>((const T*)a.x + (in ? row : 0) * H, lane, H, x);
+  load_row<T, V, LPR>((const T*)a.w, lane, H, w);
+  if (a.b) load_row<T, V, LPR>((const T*)a.b, lane, H, b);
+  float mu = 0.f;
+  if (!a.rms) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) s += x[e];
+    mu = row_sum<LPR>(s, red) * inv;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) x[e] = inside<V, LPR>(e, lane, H) ? x[e] - mu : 0.f;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPerLane; ++e) q += x[e] * x[e];
+  const float rstd = 1.f / sqrtf(row_sum<LPR>(q, red) * inv + a.eps);
+  if (!in) return;
+#pragma unroll
+  for (int e = 0; e < kPerLane; ++e) x[e] = x[e] * rstd * w[e] + (a.b ? b[e] : 0.f);
+  store_row<T, V, LPR>((T*)a.y + row * H, lane, H, x);
+  if (lane == 0) {
+    if (a.mean) a.mean[row] = mu;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
+// Each workgroup takes every gridDim.x-th set of rows and adds up its part of
+// dw and db in registers, then over its rows in LDS: one partial row each a
+// workgroup, added up by norm_bwd_reduce_kernel.
+template <typename T, int V, int LPR>
+__global__ __launch_bounds__(threads_of<LPR>) void norm_bwd_kernel(NormBwd a) {
+  constexpr int slots = threads_of<LPR> / LPR;
+  __shared__ float red[threads_of<LPR> / 64];
+  __shared__ alignas(32) float sums[slots > 1 ? NT * kPerLane : 1];
+  const int H = a.H, lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+  const float inv = 1.f / (float)H;
+  float w[kPerLane], gw[kPerLane], gb[kPerLane];
+  load_row<T, V, LPR>((const T*)a.w, lane, H, w);
+#pragma unroll
+  for (int e = 0; e < kPerLane; ++e) gw[e] = gb[e] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.N; r0 += (int64_t)gridDim.x * slots) {  // uniform
+    const int64_t row = r0 + slot;
+    const bool in = row < a.N;
+    float x[kPerLane], gy[kPerLane];
+    load_row<T, V, LPR>((const T*)a.x + (in ? row : 0) * H, lane, in ? H : 0, x);
+    load_row<T, V, LPR>((const T*)a.gy + (in ? row : 0) * H, lane, in ? H : 0, gy);
+    const float rstd = in ? a.rstd[row] : 0.f, mu = a.rms || !in ? 0.f : a.mean[row];
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) {
+      x[e] = inside<V, LPR>(e, lane, H) ? (x[e] - mu) * rstd : 0.f;
+      const float c = gy[e] * w[e];
+      s += c;
+      q += c * x[e];
+      gw[e] += gy[e] * x[e];
+      gb[e] += gy[e];
+    }
+    if (!a.gx) continue;
+    const float mc = a.rms ? 0.f : row_sum<LPR>(s, red) * inv;
+    const float mq = row_sum<LPR>(q, red) * inv;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) x[e] = rstd * (gy[e] * w[e] - mc - x[e] * mq);
+    if (in) store_row<T, V, LPR>((T*)a.gx + row * H, lane, H, x);
+  }
+  if (!a.part) return;
+  float* out = a.part + (int64_t)blockIdx.x * H;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {  // dw, then db
+    if (slots == 1) {
+      store_row<float, V, LPR>(out, lane, H, k ? gb : gw);
+    } else {
+      __syncthreads();
+      store_row<float, V, LPR>(sums + slot * H, lane, H, k ? gb : gw);
+      __syncthreads();
+      for (int d = threadIdx.x; d < H; d += NT) {
+        float t = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < slots; ++i) t += sums[i * H + d];
+        out[d] = t;
+      }
+    }
+    out += (int64_t)gridDim.x * H;
+  }
+}
+
+// Longer rows: one workgroup a row, the row read again for each pass.
 template <typename T>
 __global__ __launch_bounds__(NT) void norm_fwd_any_kernel(NormFwd a) {
   __shared__ float red[NT / 64];
@@ -106,52 +289,118 @@ __global__ __launch_bounds__(NT) void norm_bwd_w_any_kernel(NormBwd a, int group
   a.part[((int64_t)groups + blockIdx.y) * H + d] = gb;
 }
 
-// dw and db: the groups' partial sums added in a fixed order, 64 columns a
-// workgroup, four groups of partials at a time.
+// dw and db: the groups' partial sums added in a fixed order, 32 columns a
+// workgroup, 32 groups of partials side by side.
+constexpr int kReduceCols = 32, kReduceRows = 32;
 template <typename T>
-__global__ __launch_bounds__(NT) void norm_bwd_reduce_kernel(const float* part, int groups, int H, T* gw, T* gb) {
-  __shared__ float red[NT];
-  const int d = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
+__global__ __launch_bounds__(kReduceCols* kReduceRows) void norm_bwd_reduce_kernel(const float* part, int groups, int H,
+                                                                                   T* gw, T* gb) {
+  __shared__ float red[kReduceRows][kReduceCols + 1];
+  const int col = threadIdx.x % kReduceCols, k = threadIdx.x / kReduceCols;
+  const int d = blockIdx.x * kReduceCols + col;
   T* out = blockIdx.y ? gb : gw;
   if (!out) return;
   const float* p = part + (int64_t)blockIdx.y * groups * H;
   float s = 0.f;
-  if (d < H)
-    for (int g = k; g < groups; g += 4) s += p[(int64_t)g * H + d];
-  red[threadIdx.x] = s;
+  if (d < H) {
+#pragma unroll 8
+    for (int g = k; g < groups; g += kReduceRows) s += p[(int64_t)g * H + d];
+  }
+  red[k][col] = s;
   __syncthreads();
-  if (k == 0 && d < H)
-    out[d] = (T)((red[threadIdx.x] + red[64 + threadIdx.x]) + (red[128 + threadIdx.x] + red[192 + threadIdx.x]));
+  if (threadIdx.x < kReduceCols && d < H) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kReduceRows; ++i) s += red[i][col];
+    out[d] = (T)s;
+  }
 }
 
-}  // namespace
+// Lanes that share a row of H.
+int lanes_of(int H) {
+  int l = 8;
+  while (l * kPerLane < H) l *= 2;
+  return l;
+}
 
-int norm_bwd_groups(int64_t N, int H) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, (N + 15) / 16)); }
+template <typename... P>
+bool aligned16(P... p) {
+  return (((uintptr_t)p | ...) & 15) == 0;
+}
 
-namespace {
+// f(std::integral_constant<int, LPR>) for the row's lanes.
+template <typename F>
+hipError_t with_lanes(int H, F f) {
+  switch (lanes_of(H)) {
+    case 8: return f(std::integral_constant<int, 8>());
+    case 16: return f(std::integral_constant<int, 16>());
+    case 32: return f(std::integral_constant<int, 32>());
+    case 64: return f(std::integral_constant<int, 64>());
+    case 128: return f(std::integral_constant<int, 128>());
+    case 256: return f(std::integral_constant<int, 256>());
+    case 512: return f(std::integral_constant<int, 512>());
+    default: return f(std::integral_constant<int, 1024>());
+  }
+}
+
+template <typename T, int V>
+hipError_t norm_fwd_rows(const NormFwd& a, hipStream_t st) {
+  return with_lanes(a.H, [&](auto lanes) {
+    constexpr int LPR = decltype(lanes)::value, slots = threads_of<LPR> / LPR;
+    norm_fwd_kernel<T, V, LPR><<<(unsigned)((a.N + slots - 1) / slots), threads_of<LPR>, 0, st>>>(a);
+    return hipGetLastError();
+  });
+}
+
+template <typename T, int V>
+hipError_t norm_bwd_rows(const NormBwd& a, int groups, hipStream_t st) {
+  return with_lanes(a.H, [&](auto lanes) {
+    constexpr int LPR = decltype(lanes)::value;
+    norm_bwd_kernel<T, V, LPR><<<groups, threads_of<LPR>, 0, st>>>(a);
+    return hipGetLastError();
+  });
+}
 
 template <typename T>
 hipError_t norm_fwd(const NormFwd& a, hipStream_t st) {
-  norm_fwd_any_kernel<T><<<(unsigned)std::min<int64_t>(a.N, 65536), NT, 0, st>>>(a);
-  return hipGetLastError();
+  constexpr int V = 16 / sizeof(T);
+  if (a.H > kMaxLanes * kPerLane) {
+    norm_fwd_any_kernel<T><<<(unsigned)std::min<int64_t>(a.N, 65536), NT, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  return a.H % V == 0 && aligned16(a.x, a.w, a.b, a.y) ? norm_fwd_rows<T, V>(a, st) : norm_fwd_rows<T, 1>(a, st);
 }
 
 template <typename T>
 hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
-  if (a.gx && a.N > 0) {
-    norm_bwd_x_any_kernel<T><<<(unsigned)std::min<int64_t>(a.N, 65536), NT, 0, st>>>(a);
-    if (hipError_t e = hipGetLastError()) return e;
+  constexpr int V = 16 / sizeof(T);
+  const int groups = norm_bwd_groups(a.N, a.H);
+  if (a.H > kMaxLanes * kPerLane) {
+    if (a.gx && a.N > 0) {
+      norm_bwd_x_any_kernel<T><<<(unsigned)std::min<int64_t>(a.N, 65536), NT, 0, st>>>(a);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (a.part) {
+      norm_bwd_w_any_kernel<T><<<dim3((a.H + NT - 1) / NT, groups), NT, 0, st>>>(a, groups);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+  } else if (a.N > 0 || a.part) {
+    const hipError_t e = a.H % V == 0 && aligned16(a.x, a.w, a.gy, a.gx, a.part) ? norm_bwd_rows<T, V>(a, groups, st)
+                                                                                 : norm_bwd_rows<T, 1>(a, groups, st);
+    if (e != hipSuccess) return e;
   }
-  if (a.gw || a.gb) {
-    const int groups = norm_bwd_groups(a.N, a.H);
-    norm_bwd_w_any_kernel<T><<<dim3((a.H + NT - 1) / NT, groups), NT, 0, st>>>(a, groups);
-    if (hipError_t e = hipGetLastError()) return e;
-    norm_bwd_reduce_kernel<T><<<dim3((a.H + 63) / 64, 2), NT, 0, st>>>(a.part, groups, a.H, (T*)a.gw, (T*)a.gb);
-  }
+  if (a.part)
+    norm_bwd_reduce_kernel<T><<<dim3((a.H + kReduceCols - 1) / kReduceCols, 2), kReduceCols * kReduceRows, 0, st>>>(
+        a.part, groups, a.H, (T*)a.gw, (T*)a.gb);
   return hipGetLastError();
 }
 
 }  // namespace
+
+int norm_bwd_groups(int64_t N, int H) {
+  const int lanes = lanes_of(H), slots = lanes < NT ? NT / lanes : 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(512, (N + slots - 1) / slots));
+}
 
 hipError_t launch_norm_fwd(const NormFwd& a, hipStream_t st) {
   return a.dtype == 0 ? norm_fwd<float>(a, st) : norm_fwd<__bf16>(a, st);

@@ -33,7 +33,7 @@ bool in_unit(double b) { return b >= 0.0 && b < 1.0; }
 
 int check_adamw_tensor(const plp_adamw_tensor& t, int i) {
   if (t.numel < 0 || t.numel > kMaxAdamNumel)
-    return fail(PLP_E_INVALID, "tensor %d: numel=%lld outside [0, 2^35]", i, (long long)t.numel);
+    return fail(PLP_E_INVALID, "tensor %d: numel=%lld outside [0, 2^33]", i, (long long)t.numel);
   if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype))
     return fail(PLP_E_INVALID, "tensor %d: unknown dtype (param %d, grad %d)", i, t.param_dtype, t.grad_dtype);
   if (t.state_bits != 8 && t.state_bits != 32)
@@ -140,8 +140,8 @@ PLP_API int plp_layer_norm_bwd(const void* grad_y, const void* x, const void* we
   }
   rc = check_ws(ws, ws_bytes, grad_weight || grad_bias ? need : 0);
   if (rc) return rc;
-  HIP_TRY(launch_norm_bwd(NormBwd{grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias, (float*)ws, N, H,
-                                  dtype, rms ? 1 : 0},
+  HIP_TRY(launch_norm_bwd(NormBwd{grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
+                                  grad_weight || grad_bias ? (float*)ws : nullptr, N, H, dtype, rms ? 1 : 0},
                           st));
   return ok();
 }

@@ -21,7 +21,7 @@ struct NormFwd {
 hipError_t launch_norm_fwd(const NormFwd& a, hipStream_t st);
 
 // The gradients of that; gx, gw and gb may each be NULL. part: 2 x
-// norm_bwd_groups(N, H) x H floats when gw or gb is asked for.
+// norm_bwd_groups(N, H) x H floats when gw or gb is asked for, else NULL.
 struct NormBwd {
   const void *gy, *x, *w;
   const float *mean, *rstd;
@@ -48,10 +48,10 @@ struct AdamTensor {
   uint8_t param_bf16, grad_bf16, bits8, wide;  // wide: every array 16-byte aligned
 };
 constexpr int kAdamBlock = 256;   // elements of one scale
-constexpr int kAdamTile = 4096;   // elements a workgroup takes
+constexpr int kAdamTile = 1024;   // elements a workgroup takes
 // Tensors of one launch: the table goes by value in the kernel's arguments,
 // which hold 4 KB.
-constexpr int kAdamMaxTensors = 40;
+constexpr int kAdamMaxTensors = 52;
 struct AdamLaunch {
   AdamTensor t[kAdamMaxTensors];
   uint32_t first[kAdamMaxTensors + 1];  // the workgroup each tensor begins at
