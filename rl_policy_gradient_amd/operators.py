@@ -10,18 +10,18 @@ enqueued on the current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence, Union
 
 import torch
 
 from . import _abi
-from ._marshal import _check_vec, _dtype_code, _one_device, _ptr, _stream, _workspace
+from ._marshal import _check_vec, _dtype_code, _on, _one_device, _ptr, _stream_on, _workspace
 
 
 def _out(out: Optional[dict], name: str, shape, dtype, dev) -> torch.Tensor:
     """out[name], checked, or a new tensor."""
-    t = None if out is None else out.get(name)
-    if t is None:
+    if out is None or (t := out.get(name)) is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
         raise ValueError(f"out[{name!r}]: expected {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} "
@@ -46,7 +46,7 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
     N, V = (int(n) for n in logits.shape)
     rows = {k: t for k, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)) if
             isinstance(t, torch.Tensor)}
-    dev = _one_device(logits=logits, uniforms=uniforms, **rows)
+    dev = _one_device((("logits", logits), ("uniforms", uniforms), ("workspace", workspace), *rows.items()))
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("plp needs each row of logits contiguous")
     _check_vec(uniforms, N, torch.float32, "uniforms")
@@ -75,24 +75,20 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
     L = _abi.lib()
     n = ctypes.c_size_t()
     _abi.check(L.plp_sample_tokens_workspace_size(N, V, ctypes.byref(n)))
-    with torch.cuda.device(dev):
+    with _on(dev):
         res = {"token": _out(out, "token", (N,), torch.int64, dev), "logp": _out(out, "logp", (N,), torch.float32, dev),
                "kept_logp": _out(out, "kept_logp", (N,), torch.float32, dev)}
         a.token_out, a.logp_out, a.kept_logp_out = _ptr(res["token"]), _ptr(res["logp"]), _ptr(res["kept_logp"])
         ws = _workspace(n.value, dev, workspace)
-        _abi.check(L.plp_sample_tokens(ctypes.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(dev)))
+        _abi.check(L.plp_sample_tokens(ctypes.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev)))
     return res
 
 
 def _norm_sizes(x, weight, bias):
-    if x.dim() < 1:
-        raise ValueError("x needs at least one dimension")
-    H = int(x.shape[-1])
-    N = 1
-    for n in x.shape[:-1]:
-        N *= int(n)
+    *rows, H = x.shape
+    N = math.prod(rows)
     for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None and (tuple(t.shape) != (H,) or t.dtype != x.dtype):
+        if t is not None and (t.shape != (H,) or t.dtype != x.dtype):
             raise ValueError(f"{name}: expected ({H},) {x.dtype}, got {tuple(t.shape)} {t.dtype}")
     return N, H
 
@@ -103,15 +99,17 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     rms=True leaves the mean out (root-mean-square norm). weight and bias [H]
     of x's dtype (float32 or bfloat16). Returns {"y": like x, "mean" (not with
     rms), "rstd": fp32 [...]}, written into out's tensors where it has them."""
-    dev = _one_device(x=x, weight=weight, bias=bias)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    dev = _one_device((("x", x), ("weight", weight), ("bias", bias)))
     N, H = _norm_sizes(x, weight, bias)
-    with torch.cuda.device(dev):
+    with _on(dev):
         res = {"y": _out(out, "y", x.shape, x.dtype, dev), "rstd": _out(out, "rstd", x.shape[:-1], torch.float32, dev)}
         if not rms:
             res["mean"] = _out(out, "mean", x.shape[:-1], torch.float32, dev)
         _abi.check(_abi.lib().plp_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), N, H, _dtype_code(x),
                                                  1 if rms else 0, float(eps), _ptr(res["y"]), _ptr(res.get("mean")),
-                                                 _ptr(res["rstd"]), _stream(dev)))
+                                                 _ptr(res["rstd"]), _stream_on(dev)))
     return res
 
 
@@ -123,7 +121,8 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
     (plp_layer_norm_bwd); mean is required unless rms. Returns the asked-for
     ones of {"grad_x": like x, "grad_weight": [H], "grad_bias": [H]} in x's
     dtype, written into out's tensors where it has them."""
-    dev = _one_device(grad_y=grad_y, x=x, weight=weight, rstd=rstd, mean=mean)
+    dev = _one_device((("grad_y", grad_y), ("x", x), ("weight", weight), ("rstd", rstd), ("mean", mean),
+                       ("workspace", workspace)))
     N, H = _norm_sizes(x, weight, None)
     if grad_y.shape != x.shape or grad_y.dtype != x.dtype:
         raise ValueError(f"grad_y: expected {tuple(x.shape)} {x.dtype}, got {tuple(grad_y.shape)} {grad_y.dtype}")
@@ -135,7 +134,7 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
     n = ctypes.c_size_t()
     dt = _dtype_code(x)
     _abi.check(L.plp_layer_norm_bwd_workspace_size(N, H, dt, ctypes.byref(n)))
-    with torch.cuda.device(dev):
+    with _on(dev):
         res = {}
         if grad_x:
             res["grad_x"] = _out(out, "grad_x", x.shape, x.dtype, dev)
@@ -146,7 +145,7 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
         _abi.check(L.plp_layer_norm_bwd(_ptr(grad_y), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), N, H, dt,
                                         1 if rms else 0, _ptr(res.get("grad_x")), _ptr(res.get("grad_weight")),
                                         _ptr(res.get("grad_bias")), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                        _stream(dev)))
+                                        _stream_on(dev)))
     return res
 
 
@@ -217,7 +216,7 @@ def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], s
         if g.numel() != n:
             raise ValueError(f"grads[{i}]: {g.numel()} elements, the parameter has {n}")
         written = {"params": p, **{k: st[k] for k in want}}
-        d = _one_device(grads=g, **written)
+        d = _one_device((("grads", g), *written.items()))
         if dev is not None and d != dev:
             raise ValueError(f"tensor {i} is on {d}, the first on {dev}")
         dev = d
@@ -274,5 +273,5 @@ def adamw_step(table: AdamWTable, *, lr: Union[float, torch.Tensor], step: Union
     if table.count == 0:
         _abi.check(L.plp_adamw_step(ctypes.byref(a), table._array, 0, None))
         return
-    with torch.cuda.device(table.device):
-        _abi.check(L.plp_adamw_step(ctypes.byref(a), table._array, table.count, _stream(table.device)))
+    with _on(table.device):
+        _abi.check(L.plp_adamw_step(ctypes.byref(a), table._array, table.count, _stream_on(table.device)))
