@@ -30,6 +30,8 @@ namespace plp {
 
 namespace {
 
+typedef unsigned long long u64;
+
 constexpr int kChunk = 8;                       // consecutive logits a lane takes
 constexpr int kLanes = kSampleBlock / kChunk;   // lanes of one block: 32
 static_assert(kLanes == 32, "half a wave a block");
@@ -53,6 +55,77 @@ __device__ __forceinline__ double exp2_neg(double y) {
   p = fma(p, f, 1.0);
   return ldexp(p, (int)n);
 }
+
+// A value that is the same in every lane, kept in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
+__device__ __forceinline__ u64 uniform(u64 v) {
+  return (u64)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v);
+}
+__device__ __forceinline__ double uniform(double v) {
+  return __longlong_as_double((long long)uniform((u64)__double_as_longlong(v)));
+}
+// Lane `l`'s value, l the same in every lane.
+__device__ __forceinline__ int lane_of(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int l) { return (uint32_t)lane_of((int)v, l); }
+__device__ __forceinline__ float lane_of(float v, int l) { return __int_as_float(lane_of(__float_as_int(v), l)); }
+__device__ __forceinline__ u64 lane_of(u64 v, int l) {
+  return (u64)(uint32_t)lane_of((int)(v >> 32), l) << 32 | (uint32_t)lane_of((int)v, l);
+}
+__device__ __forceinline__ double lane_of(double v, int l) {
+  return __longlong_as_double((long long)lane_of((u64)__double_as_longlong(v), l));
+}
+// The value of another lane by a lane permutation (no LDS round trip); 0 where
+// it has no source or the row is not in ROWS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int permuted(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t permuted(uint32_t v) {
+  return (uint32_t)permuted<CTRL, ROWS>((int)v);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float permuted(float v) {
+  return __int_as_float(permuted<CTRL, ROWS>(__float_as_int(v)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 permuted(u64 v) {
+  return (u64)(uint32_t)permuted<CTRL, ROWS>((int)(v >> 32)) << 32 | (uint32_t)permuted<CTRL, ROWS>((int)v);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double permuted(double v) {
+  return __longlong_as_double((long long)permuted<CTRL, ROWS>((u64)__double_as_longlong(v)));
+}
+// op over the 16 lanes of a row, in each of them.
+template <typename V_, typename F>
+__device__ __forceinline__ V_ row_reduce(V_ v, F op) {
+  v = op(v, permuted<0xb1, 0xf>(v));   // lanes 1 0 3 2 of each quad
+  v = op(v, permuted<0x4e, 0xf>(v));   // lanes 2 3 0 1
+  v = op(v, permuted<0x141, 0xf>(v));  // mirrored in each half row
+  return op(v, permuted<0x140, 0xf>(v));
+}
+// op over the 32 lanes of a half wave, in each of them, and over a wave.
+template <typename V_, typename F>
+__device__ __forceinline__ V_ half_reduce(V_ v, F op) {
+  v = row_reduce(v, op);
+  return op(v, __shfl_xor(v, 16, 64));
+}
+template <typename V_, typename F>
+__device__ __forceinline__ V_ wave_reduce(V_ v, F op) {
+  v = row_reduce(v, op);
+  return op(op(lane_of(v, 0), lane_of(v, 16)), op(lane_of(v, 32), lane_of(v, 48)));
+}
+struct Add {
+  template <typename V_>
+  __device__ __forceinline__ V_ operator()(V_ a, V_ b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct Min {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
+};
 
 // Monotone whole-number keys of the logits (no NaN): -inf is the least that
 // occurs. bf16 logits need 16 bits, fp32 ones 32.
@@ -93,7 +166,7 @@ struct Row {
   __device__ int chunks() const { return (V + lead + kChunk - 1) / kChunk; }
   __device__ int blocks() const { return (V + lead + kSampleBlock - 1) / kSampleBlock; }
   __device__ int first(int c) const { return c * kChunk - lead; }
-  __device__ void load(int c, float (&z)[kChunk]) const {
+  __device__ __forceinline__ void load(int c, float (&z)[kChunk]) const {
     const int e0 = first(c);
     if (e0 >= 0 && e0 + kChunk <= V) {
       if constexpr (sizeof(T) == 4) {
@@ -146,19 +219,15 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
     nan |= z[k] != z[k];
     m = fmaxf(m, z[k]);
   }
-  int any = nan;
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor(m, o, kLanes));
-    any |= __shfl_xor(any, o, kLanes);
-  }
+  m = half_reduce(m, Max());
+  const u64 nans = __ballot(nan);
+  const bool any = (uint32_t)(nans >> (threadIdx.x & kLanes)) != 0;
   const double rate = rate_of(temperature_of(a, row));
   const double ref = m == -INFINITY ? 0.0 : (double)m;
   double s = 0.0;
 #pragma unroll
   for (int k = 0; k < kChunk; ++k) s += exp2_neg(((double)z[k] - ref) * rate);
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor(s, o, kLanes);
+  s = half_reduce(s, Add());
   if (threadIdx.x % kLanes == 0) {
     a.block_max[row * G + b] = any ? NAN : m;
     a.block_sum[row * G + b] = s;
@@ -166,153 +235,567 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Second launch: one workgroup a row.
+// Second launch: one workgroup a row. What it reads again is decided by the
+// blocks' maxima and sums:
+//
+//  1. From them alone, a value that the cut cannot lie below: one that at
+//     least k block maxima reach, or above which the blocks that reach it hold
+//     a mass of top_p even if all their other logits were as large as it. Only
+//     the blocks that reach it (the active ones) are read.
+//  2. The logits at or above it are listed in LDS; each one's rank and the mass
+//     before it give the cut (a few), or a radix search over their places in
+//     the order does (many).
+//  3. Where they are too many to list (top_p on a flat row), a histogram of
+//     about 32768 logits of the row tells near which value the cut lies; one
+//     pass adds up what is above that neighbourhood and lists what is in it.
+//  4. Where that fails too (a large k, thousands of equal logits at the cut),
+//     the neighbourhood is narrowed by exact histograms over places, 11 bits
+//     a pass, until it can be listed.
+//
+// In each case the decision is the same whole-number one. The kernel runs once
+// through most of its code, so that its size counts: loops over a lane's eight
+// logits are not unrolled and each step has one place in the code (unrolled
+// and inlined where used it was 91 KB, and a row took two to three times as
+// long, fetching it).
 // ---------------------------------------------------------------------------
-constexpr int NT = 512;
+constexpr int NT = 1024;
 constexpr int kWaves = NT / 64;
 constexpr int kBins = 2048;
 constexpr int kBinsPer = kBins / NT;
+constexpr int kList = 4096;        // logits that can be listed
+constexpr int kRanked = NT / 4;    // up to so many, every listed logit is compared with every other
+constexpr int kDirect = 32;        // active blocks up to which top_p's candidates are listed without an estimate
+constexpr int kEstimate = 32768;   // logits of the estimate
+constexpr int kAround = 1700;      // logits listed on either side of the estimated cut
 
+// A logit's place in the order, the larger the earlier: its key, then its
+// index from the end.
+constexpr int kIndexBits = 20;
+static_assert(kSampleMaxV <= 1 << kIndexBits, "an index fits its bits");
+constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
+__device__ __forceinline__ u64 place_of(uint32_t key, int index) {
+  return (u64)key << kIndexBits | (kIndexMask - (uint32_t)index);
+}
+__device__ __forceinline__ u64 last_place(uint32_t key) { return (u64)key << kIndexBits; }
+__device__ __forceinline__ int index_at(u64 place) { return (int)(kIndexMask - ((uint32_t)place & kIndexMask)); }
+
+// Inclusive scan over the wave by lane permutations within rows of 16, then
+// across rows.
 template <typename V_>
-__device__ __forceinline__ V_ wave_scan(V_ v) {  // inclusive
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const V_ u = __shfl_up(v, o, 64);
-    if ((int)(threadIdx.x & 63) >= o) v += u;
-  }
+__device__ __forceinline__ V_ wave_scan(V_ v) {
+  v += permuted<0x111, 0xf>(v);  // one lane up within the row, two, four, eight
+  v += permuted<0x112, 0xf>(v);
+  v += permuted<0x114, 0xf>(v);
+  v += permuted<0x118, 0xf>(v);
+  v += permuted<0x142, 0xa>(v);  // the row before's last into rows 1 and 3
+  v += permuted<0x143, 0xc>(v);  // row 1's last into rows 2 and 3
   return v;
 }
 
 // Sum over the threads before this one, and over all of them. `tmp` holds a
 // value per wave.
 template <typename V_>
-__device__ V_ block_scan(V_ v, V_* tmp, V_& total) {
+__device__ __forceinline__ V_ block_scan(V_ v, V_* tmp, V_& total) {
   const V_ inc = wave_scan(v);
-  if ((threadIdx.x & 63) == 63) tmp[threadIdx.x >> 6] = inc;
+  const int wave = uniform((int)threadIdx.x >> 6);
+  if ((threadIdx.x & 63) == 63) tmp[wave] = inc;
   __syncthreads();
-  V_ before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < (int)(threadIdx.x >> 6)) before += tmp[w];
-    total += tmp[w];
-  }
+  const V_ waves = wave_scan(tmp[threadIdx.x & (kWaves - 1)]);  // the first kWaves lanes' count
+  total = lane_of(waves, kWaves - 1);
+  const V_ before = wave ? lane_of(waves, wave - 1) : (V_)0;
   __syncthreads();
-  return before + inc - v;
+  return before + (inc - v);
 }
 
-// What part of the order is kept: keys above `key`, and the first `ties` by
-// index of those equal to it.
-struct Cut {
-  uint32_t key;
-  uint32_t ties;
-};
+// f(k, z[k]) for the chunk's eight, one copy of f in the code: the registers
+// move on instead of the index.
+template <typename F>
+__device__ __forceinline__ void for_chunk(float (&z)[kChunk], F f) {
+#pragma unroll 1
+  for (int k = 0; k < kChunk; ++k) {
+    f(k, z[0]);
+    const float first = z[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kChunk; ++i) z[i] = z[i + 1];
+    z[kChunk - 1] = first;  // as they were after the last
+  }
+}
 
 struct Shared {
-  unsigned long long mass[kBins];
+  u64 list[kList];  // places
+  u64 q[kList];     // their masses
+  u64 mass[kBins];
   uint32_t count[kBins];
-  unsigned long long scan64[kWaves];
-  uint32_t scan32[kWaves];
+  u64 scan64[kWaves];
   double scand[kWaves];
-  float maxw[kWaves];
-  int nanw[kWaves];
+  uint32_t scan32[kWaves];
+  float maxw[kWaves], minw[kWaves];
+  int flag[kWaves];
   // what one thread found for all
-  uint32_t bin;
-  unsigned long long before;
-  uint32_t bin_count;
-  unsigned long long bin_mass;
-  int block;
-  unsigned long long block_target, block_ties;
+  int block, bin, edge_lo, edge_hi;
+  uint32_t n, bin_count;
+  u64 place, a, b, bin_mass, above;
 };
 
 template <typename T>
 struct RowSampler {
   const Row<T> r;
   Shared& sh;
+  float* const bmax;    // [blocks] maxima
+  u64* const bq;        // [blocks] the bits of the blocks' sums (doubles), later their kept masses
+  uint16_t* const act;  // active blocks, by index
+  const int nb;
+  const float mf;
   const double m, rate;
-  const double unit;  // 2^F
-  __device__ double weight(float z) const { return exp2_neg(((double)z - m) * rate); }
-  __device__ unsigned long long quant(float z) const { return (unsigned long long)rint(weight(z) * unit); }
+  double S, unit;       // sum of the weights; 2^F
+  double least;         // min_p, or -1
 
-  // The cut at which, from the top of the order, `target` is first reached by
-  // the count (by_mass false) or by the mass. lo: the least key that takes
-  // part. above_mass: the mass above the cut's key. If the target is never
-  // reached, everything from lo on.
-  __device__ Cut find(bool by_mass, unsigned long long target, uint32_t lo, uint32_t hi,
-                      unsigned long long& above_mass) {
-    unsigned long long above = 0, am = 0;
-    uint32_t bin_count = 0;
-    for (;;) {
-      const uint32_t range = hi - lo;
-      const int bits = 32 - __clz(range | 1);
-      const int shift = bits > 11 ? bits - 11 : 0;
-      const int nbins = (int)(range >> shift) + 1;
-      for (int i = threadIdx.x; i < kBins; i += NT) sh.mass[i] = 0, sh.count[i] = 0;
+  __device__ __forceinline__ double weight(float z) const { return exp2_neg(((double)z - m) * rate); }
+  __device__ __forceinline__ u64 quant(double w) const { return (u64)rint(w * unit); }
+  __device__ __forceinline__ float value_at(u64 place) const {
+    return Key<T>::value((uint32_t)(place >> kIndexBits));
+  }
+
+  // Of the values tried between lo and hi (each wave tries one, twice), the
+  // largest that at least k block maxima reach, or above which the blocks
+  // that reach it hold `goal` for certain; lo if none.
+  __device__ __forceinline__ float bound(float lo, float hi, bool by_count, int k, double goal) {
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+      const float step = (hi - lo) / (kWaves + 1);
+      const int w = threadIdx.x >> 6;
+      const float x = lo + (float)(w + 1) * step;
+      const double wx = weight(x);
+      double s = 0.0;
+#pragma unroll 2
+      for (int b = threadIdx.x & 63; b < nb; b += 64) {
+        const double held = fmax(__longlong_as_double((long long)bq[b]) - kSampleBlock * wx, wx);
+        s += bmax[b] >= x ? (by_count ? 1.0 : held) : 0.0;
+      }
+      s = wave_reduce(s, Add());
+      if ((threadIdx.x & 63) == 0) sh.flag[w] = s >= (by_count ? (double)k : goal);
       __syncthreads();
-      for (int c = threadIdx.x; c < r.chunks(); c += NT) {
+      // f falls with x: the last wave that says yes
+      int n = 64 - __clzll((long long)__ballot((threadIdx.x & 63) < kWaves && sh.flag[threadIdx.x & (kWaves - 1)]));
+      __syncthreads();
+      n = uniform(n);
+      if (n < kWaves) hi = lo + (float)(n + 1) * step;
+      if (n > 0) lo = lo + (float)n * step;
+    }
+    return lo;
+  }
+
+  // Lists the active blocks: those whose maximum is at least z.
+  __device__ __forceinline__ int activate(float z) {
+    const int per = (nb + NT - 1) / NT, b0 = min(nb, (int)threadIdx.x * per), b1 = min(nb, b0 + per);
+    uint32_t n = 0, total;
+    for (int b = b0; b < b1; ++b) n += bmax[b] >= z;
+    uint32_t at = block_scan(n, sh.scan32, total);
+    for (int b = b0; b < b1; ++b)
+      if (bmax[b] >= z) act[at++] = (uint16_t)b;
+    __syncthreads();
+    return uniform((int)total);
+  }
+
+  // Over the active blocks: the mass of the logits before hi in the order (in
+  // sh.above), into bq what of it min_p keeps, and into the list the places
+  // from hi to lo (sh.n of them; those past kList are only counted).
+  __device__ __forceinline__ void pass(int nact, u64 lo, u64 hi) {
+    constexpr int step = NT / kLanes;
+    for (int b = threadIdx.x; b < nb; b += NT) bq[b] = 0;
+    if (threadIdx.x == 0) sh.n = 0, sh.above = 0;
+    __syncthreads();
+    u64 above = 0;
+    const int lane = threadIdx.x % kLanes;
+    float z[kChunk], next[kChunk];
+    int b = 0, bnext = 0;
+#pragma unroll 1
+    for (int i = (int)(threadIdx.x / kLanes) - step; i < nact; i += step) {  // one block ahead
+      if (i + step < nact) {
+        bnext = act[i + step];
+        r.load(bnext * kLanes + lane, next);
+      }
+      if (i >= 0) {
+        u64 kept = 0;
+        uint32_t listed = 0;
+        const int e0 = r.first(b * kLanes + lane);
+        for_chunk(z, [&](int k, float x) {
+          const u64 place = place_of(Key<T>::of(x), e0 + k);
+          if (place > hi) {
+            const double w = weight(x);
+            const u64 q = quant(w);
+            above += q;
+            if (w >= least) kept += q;
+          } else if (place >= lo) {
+            listed |= 1u << k;
+          }
+        });
+        if (__ballot(kept != 0)) {
+          kept = half_reduce(kept, Add());
+          if (lane == 0) bq[b] = kept;
+        }
+        if (__ballot(listed != 0)) {  // one addition to the count a wave (a half at the end)
+          const uint32_t mine = (uint32_t)__popc(listed), upto = wave_scan(mine);
+          const int last = 63 - __clzll((long long)__ballot(1));
+          uint32_t at = 0;
+          if ((int)(threadIdx.x & 63) == last) at = atomicAdd(&sh.n, upto);
+          at = lane_of(at, last) + upto - mine;
+          for_chunk(z, [&](int k, float x) {
+            if (listed >> k & 1) {
+              if (at < kList) sh.list[at] = place_of(Key<T>::of(x), e0 + k);
+              ++at;
+            }
+          });
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) z[k] = next[k];
+      b = bnext;
+    }
+    if (above) atomicAdd(&sh.above, above);
+    __syncthreads();
+  }
+
+  // The least whole mass at or above p times `mass`, and at least 1.
+  __device__ static __forceinline__ u64 needed(float p, double mass) {
+    const double t = ceil(fmax((double)p, 0.0) * mass);
+    return t < 1.0 ? 1ull : (u64)t;
+  }
+
+  // The cut within the list of n, above which lies the mass `above`: kept are
+  // the first k (k >= n: no limit) of those the mass before which is below p
+  // times the mass of the first k with k_on, else of everything. False if the
+  // cut is not in the list, unless `whole`: then all of it is kept. Adds the
+  // kept ones to bq; through: the mass up to and with the cut.
+  __device__ __forceinline__ bool cut_in_list(int n, u64 above, u64 k, bool k_on, float p, double mass, bool whole,
+                                              u64& cut, u64& through) {
+    u64 mine = 0, total;
+#pragma unroll 1
+    for (int j = threadIdx.x; j < n; j += NT) {
+      const u64 q = quant(weight(value_at(sh.list[j])));
+      sh.q[j] = q;
+      mine += q;
+    }
+    block_scan(mine, sh.scan64, total);
+    total = uniform(total);
+    u64 t = ~0ull;
+    if (n <= kRanked) {
+      // every place against every other: four threads share one, each with a
+      // quarter of the list
+      const int e = threadIdx.x >> 2;
+      const bool in = e < n;
+      const u64 place = in ? sh.list[e] : 0, q = in ? sh.q[e] : 0;
+      u64 rank = 0, before = 0;
+      if (in)
+#pragma unroll 4
+        for (int j = threadIdx.x & 3; j < n; j += 4)
+          if (sh.list[j] > place) ++rank, before += sh.q[j];
+      rank += __shfl_xor(rank, 1, 64);
+      rank += __shfl_xor(rank, 2, 64);
+      before += __shfl_xor(before, 1, 64);
+      before += __shfl_xor(before, 2, 64);
+      before += above;
+      const bool one = in && (threadIdx.x & 3) == 0;
+      if (one && (rank == k - 1 || (k >= (u64)n && rank == (u64)n - 1))) sh.a = before + q;
+      __syncthreads();
+      if (p < 1.f) {
+        t = uniform(needed(p, k_on ? (double)sh.a : mass));
+        if (above >= t || (!whole && t > above + total)) return false;  // uniform
+      }
+      if (one && rank < k && before < t && (rank + 1 == (u64)n || rank + 1 >= k || before + q >= t)) {
+        sh.place = place;
+        sh.b = before + q;
+      }
+      __syncthreads();
+      cut = uniform(sh.place);
+      through = uniform(sh.b);
+    } else {
+      u64 lo = 0;
+      through = above + total;
+#pragma unroll 1
+      for (int by_mass = 0; by_mass < 2; ++by_mass) {
+        u64 target = k, got;
+        if (by_mass) {
+          if (p >= 1.f) break;
+          t = uniform(needed(p, k_on ? (double)through : mass));
+          if (above >= t || (!whole && t > above + total)) return false;  // uniform
+          if (t > above + total) break;
+          target = t - above;
+        } else if (k >= (u64)n) {
+          continue;
+        }
+        const u64 at = radix(by_mass, target, lo, got);
+        lo = at > lo ? at : lo;
+        through = above + got;
+      }
+      cut = lo;
+      if (lo == 0) {  // all of it: the last one's place
+        if (threadIdx.x == 0) sh.place = ~0ull;
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += NT) atomicMin(&sh.place, sh.list[j]);
+        __syncthreads();
+        cut = uniform(sh.place);
+      }
+    }
+#pragma unroll 1
+    for (int j = threadIdx.x; j < n; j += NT) {
+      const u64 place = sh.list[j];
+      if (place >= cut && (least <= 0.0 || weight(value_at(place)) >= least))
+        atomicAdd(&bq[(index_at(place) + r.lead) / kSampleBlock], sh.q[j]);
+    }
+    __syncthreads();
+    return true;
+  }
+
+  // One step of a search for the place at which, from the top of the order, a
+  // target is first reached: the histogram of [lo, hi] (bins of 2^shift
+  // places) is in sh.mass and sh.count. reached: the count or mass above hi.
+  // Narrows lo and hi to the bin; `am` and `an`: the mass and the count above
+  // it. False if the target is not reached.
+  __device__ __forceinline__ bool step(bool by_mass, u64 target, u64& lo, u64& hi, int shift, u64& am, u64& an) {
+    u64 c0 = 0, m0 = 0, tc, tm;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
+      c0 += sh.count[bin], m0 += sh.mass[bin];
+    }
+    // both sums in one scan: counts are below 2^20 and masses below 2^62, so
+    // each needs its own
+    c0 = an + block_scan(c0, sh.scan64, tc);
+    m0 = am + block_scan(m0, sh.scan64, tm);
+    if (uniform(target > (by_mass ? am + tm : an + tc) ? 1 : 0)) return false;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
+      const u64 c1 = c0 + sh.count[bin], m1 = m0 + sh.mass[bin];
+      if ((by_mass ? m0 : c0) < target && (by_mass ? m1 : c1) >= target) {  // one thread, one bin
+        sh.bin = bin;
+        sh.a = c0;
+        sh.b = m0;
+        sh.bin_count = sh.count[bin];
+        sh.bin_mass = sh.mass[bin];
+      }
+      c0 = c1;
+      m0 = m1;
+    }
+    __syncthreads();
+    an = uniform(sh.a);
+    am = uniform(sh.b);
+    const u64 range = hi - lo, bin = (u64)uniform(sh.bin), last = (bin << shift) | ((1ull << shift) - 1);
+    hi = lo + (last < range ? last : range);
+    lo += bin << shift;
+    return true;
+  }
+
+  __device__ __forceinline__ void clear_bins() {
+    for (int i = threadIdx.x; i < kBins; i += NT) sh.mass[i] = 0, sh.count[i] = 0;
+    __syncthreads();
+  }
+  static __device__ __forceinline__ int shift_of(u64 range) {
+    const int bits = 64 - __clzll((long long)(range | 1));
+    return bits > 11 ? bits - 11 : 0;
+  }
+
+  // Among the listed places at or above `least_place` the one at which
+  // `target` is first reached, which it is; through: the mass up to and with it.
+  __device__ __forceinline__ u64 radix(bool by_mass, u64 target, u64 least_place, u64& through) {
+    u64 lo = least_place, hi = last_place(Key<T>::of(mf)) | kIndexMask, am = 0, an = 0;
+    const int n = uniform((int)sh.n);
+#pragma unroll 1
+    for (;;) {
+      const int shift = shift_of(hi - lo);
+      clear_bins();
+#pragma unroll 1
+      for (int j = threadIdx.x; j < n; j += NT) {
+        const u64 place = sh.list[j];
+        if (place >= lo && place <= hi) {
+          atomicAdd(&sh.mass[(place - lo) >> shift], sh.q[j]);
+          atomicAdd(&sh.count[(place - lo) >> shift], 1u);
+        }
+      }
+      __syncthreads();
+      if (!step(by_mass, target, lo, hi, shift, am, an)) break;
+      const int left = uniform((int)sh.bin_count);
+      through = am + uniform(sh.bin_mass);
+      __syncthreads();
+      if (left == 1 || !shift) break;
+    }
+#pragma unroll 1
+    for (int j = threadIdx.x; j < n; j += NT)
+      if (sh.list[j] >= lo && sh.list[j] <= hi) sh.place = sh.list[j];
+    __syncthreads();
+    return uniform(sh.place);
+  }
+
+  // Narrows [lo, hi] around the place at which the count or the mass of the
+  // row first reaches the target until it can be listed; an: the logits above
+  // it. If the target is never reached, to nothing below everything.
+  __device__ __forceinline__ void narrow(bool by_mass, u64 target, u64& lo, u64& hi, u64& an) {
+    const u64 bottom = lo;
+    u64 am = 0;
+#pragma unroll 1
+    for (;;) {
+      const int shift = shift_of(hi - lo);
+      clear_bins();
+      const int chunks = r.chunks();
+#pragma unroll 1
+      for (int c = threadIdx.x; c < chunks; c += NT) {
         float z[kChunk];
         r.load(c, z);
-#pragma unroll
-        for (int k = 0; k < kChunk; ++k) {
-          const uint32_t key = Key<T>::of(z[k]);
-          if (key >= lo && key <= hi) {
-            atomicAdd(&sh.count[(key - lo) >> shift], 1u);
-            if (shift) atomicAdd(&sh.mass[(key - lo) >> shift], quant(z[k]));
+        const int e0 = r.first(c);
+        for_chunk(z, [&](int k, float x) {
+          const u64 place = place_of(Key<T>::of(x), e0 + k);
+          if (place >= lo && place <= hi) {
+            atomicAdd(&sh.mass[(place - lo) >> shift], quant(weight(x)));
+            atomicAdd(&sh.count[(place - lo) >> shift], 1u);
           }
-        }
+        });
       }
       __syncthreads();
-      if (!shift)  // one key a bin: its mass is its count times its weight
-        for (int i = threadIdx.x; i < nbins; i += NT)
-          sh.mass[i] = sh.count[i] * quant(Key<T>::value(lo + i));
-      __syncthreads();
-      unsigned long long cnt = 0, mas = 0;
-#pragma unroll
-      for (int i = 0; i < kBinsPer; ++i) {
-        const int bin = nbins - 1 - ((int)threadIdx.x * kBinsPer + i);
-        if (bin >= 0) cnt += sh.count[bin], mas += sh.mass[bin];
+      if (!step(by_mass, target, lo, hi, shift, am, an)) {
+        lo = bottom;
+        hi = bottom - 1;
+        an = 0;
+        return;
       }
-      unsigned long long tc, tm;
-      unsigned long long c0 = block_scan(cnt, sh.scan64, tc), m0 = block_scan(mas, sh.scan64, tm);
-      if (by_mass ? am + tm < target : above + tc < target) {  // never reached
-        above_mass = am + tm;
-        return Cut{lo, 0xffffffffu};
-      }
-#pragma unroll
-      for (int i = 0; i < kBinsPer; ++i) {
-        const int bin = nbins - 1 - ((int)threadIdx.x * kBinsPer + i);
-        if (bin < 0) continue;
-        const unsigned long long c1 = c0 + sh.count[bin], m1 = m0 + sh.mass[bin];
-        const unsigned long long x0 = by_mass ? am + m0 : above + c0, x1 = by_mass ? am + m1 : above + c1;
-        if (x0 < target && x1 >= target) {  // one thread, one bin
-          sh.bin = bin;
-          sh.before = c0;
-          sh.block_target = m0;
-          sh.bin_count = sh.count[bin];
-          sh.bin_mass = sh.mass[bin];
-        }
-        c0 = c1;
-        m0 = m1;
-      }
+      const int left = uniform((int)sh.bin_count);
       __syncthreads();
-      above += sh.before;
-      am += sh.block_target;
-      bin_count = sh.bin_count;
-      const uint32_t bin = sh.bin;
-      __syncthreads();
-      const uint32_t last = (bin << shift) | ((1u << shift) - 1);  // within the bracket, which may end at 2^32 - 1
-      hi = lo + (last < range ? last : range);
-      lo += bin << shift;
-      if (!shift) break;
+      if (left <= kList) return;
     }
-    above_mass = am;
-    const unsigned long long need = target - (by_mass ? am : above);  // >= 1
-    unsigned long long ties = need;
-    if (by_mass) {
-      const unsigned long long q = quant(Key<T>::value(lo));
-      ties = q ? (need + q - 1) / q : bin_count;
+  }
+
+  // Bounds of a neighbourhood of the cut, above which a mass of `t` of the
+  // row's lies, from a sample of the row in which the mass below the cut is
+  // counted from the bottom, where no single logit weighs much. Logits below
+  // zl are surely below the cut.
+  __device__ __forceinline__ void estimate(u64 t, float zl, u64& lo, u64& hi) {
+    const float scale = (float)kBins / (mf - zl), ratef = (float)rate;
+    const int chunks = r.chunks(), step = max(1, chunks * kChunk / kEstimate);
+    if (threadIdx.x == 0) sh.bin = kBins - 1, sh.bin_count = 0, sh.edge_lo = 0, sh.edge_hi = kBins;
+    clear_bins();
+    float low = 0.f;
+#pragma unroll 1
+    for (int c = threadIdx.x * step; c < chunks; c += NT * step) {
+      float z[kChunk];
+      r.load(c, z);
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k)
+        if (z[k] >= zl)
+          atomicAdd(&sh.count[min(kBins - 1, (int)((z[k] - zl) * scale))], 1u);
+        else
+          low += exp2f((z[k] - mf) * ratef);
     }
-    return Cut{lo, (uint32_t)(ties < bin_count ? ties : bin_count)};
+    __syncthreads();
+    double mass[kBinsPer], mine = 0.0, all, lows;
+    uint32_t cnt[kBinsPer], n = 0, total;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const int bin = threadIdx.x * kBinsPer + i;
+      cnt[i] = sh.count[bin];
+      mass[i] = (double)cnt[i] * (double)exp2f((zl + ((float)bin + 0.5f) / scale - mf) * ratef);
+      mine += mass[i];
+      n += cnt[i];
+    }
+    block_scan((double)low, sh.scand, lows);
+    double run = block_scan(mine, sh.scand, all);
+    const uint32_t c0 = block_scan(n, sh.scan32, total);
+    const double below = (S - (double)t / unit) / step - lows;  // of the sample, from zl on
+    uint32_t at = c0;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      if (run < below && run + mass[i] >= below) {
+        sh.bin = threadIdx.x * kBinsPer + i;
+        sh.bin_count = at;
+      }
+      run += mass[i];
+      at += cnt[i];
+    }
+    if (threadIdx.x == 0 && below <= 0.0) sh.bin = 0;
+    if (threadIdx.x == 0 && below > all) sh.bin_count = total;
+    __syncthreads();
+    // edges: kAround logits below the cut's bin and above it
+    const int around = kAround / step;
+    const int lo_at = (int)sh.bin_count - around, hi_at = (int)(sh.bin_count + sh.count[sh.bin]) + around;
+    at = c0;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const int bin = threadIdx.x * kBinsPer + i;
+      if ((int)at <= lo_at && (int)(at + cnt[i]) > lo_at) sh.edge_lo = bin;
+      if ((int)at < hi_at && (int)(at + cnt[i]) >= hi_at) sh.edge_hi = bin + 1;
+      at += cnt[i];
+    }
+    __syncthreads();
+    const int edge_lo = uniform(sh.edge_lo), edge_hi = uniform(sh.edge_hi);
+    if (edge_lo > 0) lo = last_place(Key<T>::of(zl + (float)edge_lo / scale));
+    if (edge_hi < kBins) hi = last_place(Key<T>::of(zl + (float)edge_hi / scale)) - 1;
+  }
+
+  // The cut's place, and the blocks' kept masses in bq, which holds the
+  // blocks' sums (relative to m) on entry.
+  __device__ __forceinline__ u64 cut(int top_k, float top_p, float lowest_max) {
+    const bool k_on = top_k > 0 && top_k < r.V, p_on = top_p < 1.f;
+    const uint32_t lowest = Key<T>::of(-INFINITY) + 1;  // the least finite key
+    const float all = Key<T>::value(lowest);
+    float L = all, from = lowest_max;
+    double goal = 0.0;
+    if (!k_on && p_on) {
+      goal = (double)top_p * S * (1.0 + 1e-9);
+      // with every other logit at most (1 - p) S / (2 x their number), it holds
+      from = fmaxf(all, (float)(m + log2((1.0 - (double)fmaxf(top_p, 0.f)) * S / (512.0 * nb)) / rate));
+    }
+    if (k_on ? top_k <= nb : p_on) L = bound(from, mf, k_on, top_k, goal);
+    bool whole = false;  // whether what lies below L is cut by min_p, whatever the mass above it
+    if (!k_on && least > 0.0) {
+      const double z = m + (log2(least) - 1e-6) / rate;  // below it, w < min_p for certain
+      uint32_t key = Key<float>::of((float)z);
+      if ((double)Key<float>::value(key) > z) --key;
+      const float zm = Key<float>::value(key);
+      whole = zm >= L;
+      L = fmaxf(L, zm);
+    }
+    L = uniform(L);
+    int nact = activate(L);
+    if (k_on && nact < top_k) nact = activate(L = all);  // fewer blocks than k, or than k that hold anything
+    u64 place = last_place(lowest), through = 0;
+    double mass = S * unit;
+    u64 k = k_on ? (u64)top_k : ~0ull;
+    bool count = k_on;  // the first k are still to be found
+    const bool limits = k_on || p_on;
+    // 0: list all candidates; 1: those around an estimate of the cut; 2: narrow
+#pragma unroll 1
+    for (int method = k_on || !limits || nact <= kDirect || !(L < mf) ? 0 : 1; method < 3; ++method) {
+      if (method == 1 && (k_on || !(L < mf))) continue;
+      if (method == 2) nact = activate(all);
+      const u64 bottom = last_place(max(lowest, Key<T>::of(method == 2 ? all : L)));
+      u64 lo = bottom, hi = last_place(Key<T>::of(mf)) | kIndexMask;
+      u64 an = 0;
+      if (!limits) hi = lo - 1;
+      if (method == 1) estimate(needed(top_p, mass), L, lo, hi);
+      const bool one_limit = method == 2 && count && p_on;  // k's cut first, then top_p's
+      if (method == 2) narrow(!count, count ? k : needed(top_p, mass), lo, hi, an);
+      pass(nact, lo, hi);
+      const int n = uniform((int)sh.n);
+      const u64 above = uniform(sh.above);
+      if (!limits) return place;
+      if (method == 2 && hi < lo) {  // never reached: everything
+        if (!one_limit) return place;
+        mass = (double)above;
+        count = false;
+        method = 1;
+        k = ~0ull;
+        continue;
+      }
+      if (n == 0 || n > kList) continue;
+      if (!cut_in_list(n, above, k == ~0ull ? k : k - an, count, one_limit ? 1.f : top_p, mass, whole && lo == bottom, place,
+                       through))
+        continue;
+      if (!one_limit) return place;
+      mass = (double)through;
+      count = false;
+      method = 1;
+      k = ~0ull;
+    }
+    return place;
   }
 };
 
@@ -320,13 +803,12 @@ template <typename T>
 __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
   extern __shared__ char lds[];
   Shared& sh = *reinterpret_cast<Shared*>(lds);
-  unsigned long long* bq = reinterpret_cast<unsigned long long*>(lds + sizeof(Shared));  // [G] kept mass
-  uint32_t* bt = reinterpret_cast<uint32_t*>(bq + G);                                    // [G] ties
+  u64* bq = reinterpret_cast<u64*>(lds + sizeof(Shared));
+  float* bmax = reinterpret_cast<float*>(bq + G);
+  uint16_t* act = reinterpret_cast<uint16_t*>(bmax + G);
   const int64_t row = blockIdx.x;
   const Row<T> r(a, row);
   const int nb = r.blocks();
-  const float* bmax = a.block_max + row * G;
-  const double* bsum = a.block_sum + row * G;
 
   const float tau = temperature_of(a, row);
   const float top_p = a.top_p_rows ? a.top_p_rows[row] : a.top_p;
@@ -334,22 +816,32 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
   const int top_k = a.top_k_rows ? a.top_k_rows[row] : a.top_k;
   float u = a.uniforms[row];
 
-  float mf = -INFINITY;
+  // the largest logit, the least finite maximum of a block, and whether any is NaN
+  float mf = -INFINITY, lowest_max = INFINITY;
   int nan = 0;
+#pragma unroll 1
   for (int b = threadIdx.x; b < nb; b += NT) {
-    const float v = bmax[b];
+    const float v = a.block_max[row * G + b];
+    bmax[b] = v;
+    bq[b] = (u64)__double_as_longlong(a.block_sum[row * G + b]);
     nan |= v != v;
     mf = fmaxf(mf, v);
+    if (v > -INFINITY) lowest_max = fminf(lowest_max, v);
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    mf = fmaxf(mf, __shfl_xor(mf, o, 64));
-    nan |= __shfl_xor(nan, o, 64);
+  mf = wave_reduce(mf, Max());
+  lowest_max = wave_reduce(lowest_max, Min());
+  nan = __ballot(nan) != 0;
+  if ((threadIdx.x & 63) == 0) {
+    sh.maxw[threadIdx.x >> 6] = mf;
+    sh.minw[threadIdx.x >> 6] = lowest_max;
+    sh.flag[threadIdx.x >> 6] = nan;
   }
-  if ((threadIdx.x & 63) == 0) sh.maxw[threadIdx.x >> 6] = mf, sh.nanw[threadIdx.x >> 6] = nan;
+  if (threadIdx.x == 0) sh.block = 0x7fffffff, sh.bin = 0x7fffffff;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) mf = fmaxf(mf, sh.maxw[w]), nan |= sh.nanw[w];
+  static_assert(kWaves == 16, "a row of lanes holds the waves' values");
+  mf = uniform(row_reduce(sh.maxw[threadIdx.x & (kWaves - 1)], Max()));
+  lowest_max = uniform(row_reduce(sh.minw[threadIdx.x & (kWaves - 1)], Min()));
+  nan = __ballot(sh.flag[threadIdx.x & (kWaves - 1)]) != 0;
   __syncthreads();
   // no distribution: a NaN, nothing above -inf, +inf, or a setting that is none
   if (nan || !(fabsf(mf) < INFINITY) || !(tau >= 0.f && tau < INFINITY) || top_p != top_p || min_p != min_p ||
@@ -362,178 +854,84 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
     return;
   }
   if (tau == 0.f) {  // the first of the largest
-    if (threadIdx.x == 0) sh.block = 0x7fffffff;
-    __syncthreads();
     for (int b = threadIdx.x; b < nb; b += NT)
-      if (bmax[b] == mf) {
-        atomicMin(&sh.block, b);
-        break;
-      }
+      if (bmax[b] == mf) atomicMin(&sh.block, b);
     __syncthreads();
-    if (threadIdx.x < kLanes) {
-      const int c = sh.block * kLanes + threadIdx.x;
-      float z[kChunk];
-      r.load(c, z);
-      int at = 0x7fffffff;
-#pragma unroll
-      for (int k = kChunk - 1; k >= 0; --k)
-        if (z[k] == mf) at = r.first(c) + k;
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) at = min(at, __shfl_xor(at, o, kLanes));
-      if (threadIdx.x == 0) {
-        a.token[row] = at;
-        if (a.logp) a.logp[row] = 0.f;
-        if (a.kept_logp) a.kept_logp[row] = 0.f;
-      }
+    const int e = sh.block * kSampleBlock - r.lead + (int)threadIdx.x;
+    if (threadIdx.x < kSampleBlock && e >= 0 && e < r.V && (float)r.p[e] == mf) atomicMin(&sh.bin, e);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      a.token[row] = sh.bin;
+      if (a.logp) a.logp[row] = 0.f;
+      if (a.kept_logp) a.kept_logp[row] = 0.f;
     }
     return;
   }
 
-  const double rate = rate_of(tau);
+  RowSampler<T> s{r, sh, bmax, bq, act, nb, mf, uniform((double)mf), uniform(rate_of(tau)), 0.0, 0.0,
+                  uniform(min_p > 0.f ? fmin((double)min_p, 1.0) : -1.0)};
   const int per = (nb + NT - 1) / NT;  // blocks a thread takes, one after the other
   const int b0 = min(nb, (int)threadIdx.x * per), b1 = min(nb, b0 + per);
   double sum = 0.0;
-  for (int b = b0; b < b1; ++b) sum += bsum[b] * exp2_neg(((double)bmax[b] - (double)mf) * rate);
-  double S;
-  block_scan(sum, sh.scand, S);
-  // q_i = round(w_i 2^F) add up to less than 2^62: S < 2^(e+1), and the
-  // roundings add at most half of V <= 2^20
-  const int F = 60 - ilogb(S);
-  RowSampler<T> s{r, sh, (double)mf, rate, ldexp(1.0, F)};
-
-  const uint32_t lowest = Key<T>::of(-INFINITY) + 1, highest = Key<T>::of(mf);
-  Cut cut{lowest, 0xffffffffu};
-  const bool k_on = top_k > 0 && top_k < a.V, p_on = top_p < 1.f, m_on = min_p > 0.f;
-  unsigned long long above = 0;
-  if (k_on) cut = s.find(false, top_k, lowest, highest, above);
-  if (p_on) {
-    double mass;
-    if (k_on) {
-      const unsigned long long q = s.quant(Key<T>::value(cut.key));
-      mass = cut.ties == 0xffffffffu ? (double)above : (double)above + (double)cut.ties * (double)q;
-    } else {
-      mass = S * s.unit;
-    }
-    const double t = ceil(fmax((double)top_p, 0.0) * mass);
-    unsigned long long ap;
-    const Cut c = s.find(true, t < 1.0 ? 1ull : (unsigned long long)t, k_on ? cut.key : lowest, highest, ap);
-    if (!k_on || c.key > cut.key || (c.key == cut.key && c.ties < cut.ties)) cut = c;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const double w = __longlong_as_double((long long)bq[b]) * s.weight(bmax[b]);
+    bq[b] = (u64)__double_as_longlong(w);
+    sum += w;
   }
-  const bool limited = k_on || p_on || m_on;
-  const double least = fmin((double)min_p, 1.0);
-
-  // the kept mass of each block, and its ties with the cut
-  if (limited) {
-    for (int b = threadIdx.x / kLanes; b < nb; b += NT / kLanes) {
-      float z[kChunk];
-      r.load(b * kLanes + threadIdx.x % kLanes, z);
-      unsigned long long q = 0;
-      uint32_t t = 0;
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k) {
-        const uint32_t key = Key<T>::of(z[k]);
-        if (key < cut.key) continue;
-        if (key == cut.key && cut.ties != 0xffffffffu)
-          ++t;
-        else if (s.weight(z[k]) >= least)
-          q += s.quant(z[k]);
-      }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) q += __shfl_xor(q, o, kLanes), t += __shfl_xor(t, o, kLanes);
-      if (threadIdx.x % kLanes == 0) bq[b] = q, bt[b] = t;
-    }
-    __syncthreads();
-    uint32_t ties = 0, all;
-    for (int b = b0; b < b1; ++b) ties += bt[b];
-    uint32_t before = block_scan(ties, sh.scan32, all);
-    const float zc = Key<T>::value(cut.key);
-    const unsigned long long qc = s.weight(zc) >= least ? s.quant(zc) : 0;
-    for (int b = b0; b < b1; ++b) {
-      const uint32_t mine = bt[b], left = before < cut.ties ? cut.ties - before : 0;
-      bq[b] += (unsigned long long)(mine < left ? mine : left) * qc;
-      bt[b] = left;  // ties this block may still keep
-      before += mine;
-    }
-  } else {
+  block_scan(sum, sh.scand, s.S);
+  s.S = uniform(s.S);
+  // q = round(w 2^F) add up to less than 2^62: S < 2^(e+1), and the roundings
+  // add at most half of V <= 2^20
+  s.unit = uniform(ldexp(1.0, 60 - ilogb(s.S)));
+  u64 cut = 0;
+  const bool limited = (top_k > 0 && top_k < a.V) || top_p < 1.f || min_p > 0.f;
+  if (limited) cut = s.cut(top_k, top_p, lowest_max);
+  u64 mine = 0, total;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
     // a block whose largest logit weighs nothing is left out, so that the
     // block taken holds a token to take
-    for (int b = b0; b < b1; ++b)
-      bq[b] = s.quant(bmax[b]) ? (unsigned long long)rint(bsum[b] * s.weight(bmax[b]) * s.unit) : 0ull;
+    if (!limited) bq[b] = s.quant(s.weight(bmax[b])) ? s.quant(__longlong_as_double((long long)bq[b])) : 0ull;
+    mine += bq[b];
   }
-  unsigned long long mine = 0, total;
-  for (int b = b0; b < b1; ++b) mine += bq[b];
-  unsigned long long before = block_scan(mine, sh.scan64, total);
+  u64 before = block_scan(mine, sh.scan64, total);
   u = fminf(fmaxf(u, 0.f), 0x1.fffffep-1f);
-  const unsigned long long target = (unsigned long long)((double)u * (double)total);  // the sum to exceed
+  const u64 target = (u64)((double)u * (double)total);  // the sum to exceed
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    if (before <= target && before + bq[b] > target) sh.block = b, sh.block_target = target - before;
+    if (before <= target && before + bq[b] > target) sh.block = b, sh.a = target - before;
     before += bq[b];
   }
   __syncthreads();
 
-  // the index within the block
-  if (threadIdx.x < 64) {
-    const int l = threadIdx.x;
-    const int c = sh.block * kLanes + l;
-    float z[kChunk];
-    unsigned long long q[kChunk], chunk = 0;
-    uint32_t t = 0;
-    if (l < kLanes) r.load(c, z);
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) {
-      if (l >= kLanes) z[k] = -INFINITY;
-      t += Key<T>::of(z[k]) == cut.key;
+  // the index within the block, a thread a logit: the first at which the sum
+  // exceeds the target, or, if roundings of the block's own sum leave none,
+  // the last that weighs anything
+  const int e = sh.block * kSampleBlock - r.lead + (int)threadIdx.x;
+  float z = -INFINITY;
+  u64 q = 0, all;
+  if (threadIdx.x < kSampleBlock && e >= 0 && e < r.V) {
+    z = (float)r.p[e] + 0.f;
+    if (z > -INFINITY && place_of(Key<T>::of(z), e) >= cut) {
+      const double w = s.weight(z);
+      if (w >= s.least) q = s.quant(w);
     }
-    uint32_t rank = wave_scan(t) - t;
-    const uint32_t left = limited ? bt[sh.block] : 0;
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) {
-      const uint32_t key = Key<T>::of(z[k]);
-      bool keep = z[k] != -INFINITY;
-      if (limited) {
-        keep = keep && key >= cut.key && s.weight(z[k]) >= least;
-        if (key == cut.key && cut.ties != 0xffffffffu) keep = keep && rank++ < left;
-      }
-      q[k] = keep ? s.quant(z[k]) : 0;
-      chunk += q[k];
-    }
-    unsigned long long run = wave_scan(chunk) - chunk;
-    // the first index at which the sum exceeds the target; if roundings of
-    // the block's own sum leave none, the last that weighs anything
-    int hit = 0x7fffffff, last = -1;
-    float zh = 0.f, zl = 0.f;
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) {
-      run += q[k];
-      if (q[k]) {
-        last = r.first(c) + k, zl = z[k];
-        if (run > sh.block_target && hit == 0x7fffffff) hit = r.first(c) + k, zh = z[k];
-      }
-    }
-    const int first = [&] {
-      int x = hit;
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) x = min(x, __shfl_xor(x, o, 64));
-      return x;
-    }();
-    int end = last;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) end = max(end, __shfl_xor(end, o, 64));
-    const int tok = first != 0x7fffffff ? first : end;
-    if (hit == tok || (first == 0x7fffffff && last == tok)) {
-      const float zt = hit == tok ? zh : zl;
-      const double x = ((double)zt - (double)mf) / (double)tau;
-      a.token[row] = tok;
-      if (a.logp) a.logp[row] = (float)(x - log(S));
-      if (a.kept_logp) a.kept_logp[row] = (float)(x - log((double)total / s.unit));
-    }
+  }
+  const u64 inside = sh.a, run = block_scan(q, sh.scan64, all);
+  const u64 aim = inside < all ? inside : all - 1;  // all > 0: the block's largest logit weighs something
+  if (q && run <= aim && run + q > aim) {
+    const double x = ((double)z - (double)mf) / (double)tau;
+    a.token[row] = e;
+    if (a.logp) a.logp[row] = (float)(x - log(s.S));
+    if (a.kept_logp) a.kept_logp[row] = (float)(x - log((double)total / s.unit));
   }
 }
 
 template <typename T>
 hipError_t sample(const SampleArgs& a, hipStream_t st) {
   const int G = sample_blocks(a.V);
-  const size_t lds = sizeof(Shared) + (size_t)G * 12;
+  const size_t lds = sizeof(Shared) + (size_t)G * (sizeof(u64) + sizeof(float) + sizeof(uint16_t));
   for (int64_t r0 = 0; r0 < a.N; r0 += 32768) {  // the grid's second dimension holds 65535
     SampleArgs b = a;
     b.N = std::min<int64_t>(32768, a.N - r0);
