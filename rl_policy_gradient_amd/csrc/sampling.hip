@@ -11,9 +11,9 @@
 //
 // Every decision (which value is the cut, how many of it are kept, at which
 // index the sum is exceeded) is taken on whole numbers q_i = round(w_i 2^F),
-// F chosen so that they add up below 2^62: their sums are exact, so the
+// F chosen so that they add up below 2^52: their sums are exact, so the
 // result does not depend on the order of additions or on the launch's shape.
-// w_i is formed in fp64 (2^x by its own polynomial, to 4e-16): at a vocabulary's
+// w_i is formed in fp64 (2^x by its own polynomial, to 2e-14): at a vocabulary's
 // length an fp32 weight's rounding moves the running sum across a token of
 // the tail too often.
 //
@@ -36,25 +36,31 @@ constexpr int kChunk = 8;                       // consecutive logits a lane tak
 constexpr int kLanes = kSampleBlock / kChunk;   // lanes of one block: 32
 static_assert(kLanes == 32, "half a wave a block");
 
-// 2^y for y <= 0 (and a little above): a polynomial of degree 10 through the
-// Chebyshev points of [-1/2, 1/2] (relative error 3.2e-16) times 2^round(y).
-// Below -1100 the result is 0; not for NaN.
-__device__ __forceinline__ double exp2_neg(double y) {
-  y = fmax(y, -1100.0);
-  const double n = rint(y), f = y - n;
-  double p = 0x1.e6063f7217bc6p-28;
-  p = fma(p, f, 0x1.b675bca4eeebbp-24);
-  p = fma(p, f, 0x1.62bfd47773353p-20);
-  p = fma(p, f, 0x1.ffcb54062e698p-17);
-  p = fma(p, f, 0x1.430913096fd9fp-13);
-  p = fma(p, f, 0x1.5d87fe9d7a584p-10);
-  p = fma(p, f, 0x1.3b2ab6fba1ddap-7);
-  p = fma(p, f, 0x1.c6b08d703ce49p-5);
-  p = fma(p, f, 0x1.ebfbdff82c598p-3);
-  p = fma(p, f, 0x1.62e42fefa3a19p-1);
+// 2^(d rate) for d rate between -1000 and a little above 0 (the callers hold
+// d at or above -1000 / rate): a polynomial of degree 9 through the Chebyshev
+// points of [-1/2, 1/2] (relative error 1.9e-14) on the distance
+// to the nearest whole number, which is added to the result's exponent.
+// Adding 1.5 x 2^52 rounds to that number and leaves it in the sum's low
+// bits: no conversion, and 14 operations in all.
+__device__ __forceinline__ double exp2_of(double d, double rate) {
+  constexpr double magic = 0x1.8p52;
+  const double t = fma(d, rate, magic);
+  const double f = fma(d, rate, magic - t);
+  double p = 0x1.b6571de2f2351p-24;
+  p = fma(p, f, 0x1.63ef969a64d3cp-20);
+  p = fma(p, f, 0x1.ffcb76789860fp-17);
+  p = fma(p, f, 0x1.43088e257f341p-13);
+  p = fma(p, f, 0x1.5d87fe908f88ap-10);
+  p = fma(p, f, 0x1.3b2ab72b175eep-7);
+  p = fma(p, f, 0x1.c6b08d7044119p-5);
+  p = fma(p, f, 0x1.ebfbdff8149f2p-3);
+  p = fma(p, f, 0x1.62e42fefa39f7p-1);
   p = fma(p, f, 1.0);
-  return ldexp(p, (int)n);
+  const int n = (int)(uint32_t)__double_as_longlong(t);
+  return __hiloint2double(__double2hiint(p) + (n << 20), __double2loint(p));
 }
+// The least d that exp2_of takes: -1000 / rate.
+__device__ __forceinline__ double least_of(float tau) { return tau == 0.f ? -1000.0 : (double)tau * -693.147180559945; }
 
 // A value that is the same in every lane, kept in scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -135,7 +141,7 @@ template <>
 struct Key<float> {
   static constexpr int bits = 32;
   __device__ static uint32_t of(float z) {
-    const uint32_t b = __float_as_uint(z);
+    const uint32_t b = __float_as_uint(z + 0.f);  // -0 ties with +0
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
   }
   __device__ static float value(uint32_t k) {
@@ -154,7 +160,7 @@ struct Key<__bf16> {
 // Row `row` of the logits as chunks of 8 that begin at multiples of 16 bytes
 // of the address: chunk c holds the elements 8c - lead .. 8c - lead + 7 of the
 // row, those outside [0, V) as -inf. (A bf16 chunk is one 16-byte load, an
-// fp32 one two.) -0 becomes +0, which it ties with.
+// fp32 one two.)
 template <typename T>
 struct Row {
   const T* p;
@@ -185,8 +191,6 @@ struct Row {
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) z[k] = e0 + k >= 0 && e0 + k < V ? (float)p[e0 + k] : -INFINITY;
     }
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) z[k] += 0.f;
   }
 };
 
@@ -203,34 +207,40 @@ __device__ __forceinline__ double rate_of(float tau) { return tau == 0.f ? 1.0 :
 constexpr int kStatThreads = 256;
 constexpr int kStatBlocks = kStatThreads / kLanes;
 
+// The larger, NaN if either is.
+struct MaxOrNan {
+  __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
+};
+
+// Each half wave takes `rounds` blocks, kStatBlocks apart, the next one's
+// loads issued before the present one's arithmetic.
 template <typename T>
-__global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a, int G) {
+__global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a, int G, int rounds) {
   const int64_t row = blockIdx.y;
   const Row<T> r(a, row);
-  const int b = blockIdx.x * kStatBlocks + threadIdx.x / kLanes;
-  if (b >= r.blocks()) return;  // uniform over the half wave
-  const int c = b * kLanes + threadIdx.x % kLanes;
-  float z[kChunk];
-  r.load(c, z);
-  float m = -INFINITY;
-  bool nan = false;
+  const int nb = r.blocks(), lane = threadIdx.x % kLanes;
+  const float tau = temperature_of(a, row);
+  const double rate = rate_of(tau), least = least_of(tau);
+  int b = blockIdx.x * rounds * kStatBlocks + threadIdx.x / kLanes;
+  float z[kChunk], next[kChunk];
+  if (b < nb) r.load(b * kLanes + lane, next);
+  for (int i = 0; i < rounds && b < nb; ++i, b += kStatBlocks) {  // uniform over the half wave
 #pragma unroll
-  for (int k = 0; k < kChunk; ++k) {
-    nan |= z[k] != z[k];
-    m = fmaxf(m, z[k]);
-  }
-  m = half_reduce(m, Max());
-  const u64 nans = __ballot(nan);
-  const bool any = (uint32_t)(nans >> (threadIdx.x & kLanes)) != 0;
-  const double rate = rate_of(temperature_of(a, row));
-  const double ref = m == -INFINITY ? 0.0 : (double)m;
-  double s = 0.0;
+    for (int k = 0; k < kChunk; ++k) z[k] = next[k];
+    if (i + 1 < rounds && b + kStatBlocks < nb) r.load((b + kStatBlocks) * kLanes + lane, next);
+    float m = z[0];
 #pragma unroll
-  for (int k = 0; k < kChunk; ++k) s += exp2_neg(((double)z[k] - ref) * rate);
-  s = half_reduce(s, Add());
-  if (threadIdx.x % kLanes == 0) {
-    a.block_max[row * G + b] = any ? NAN : m;
-    a.block_sum[row * G + b] = s;
+    for (int k = 1; k < kChunk; ++k) m = MaxOrNan()(m, z[k]);
+    m = half_reduce(m, MaxOrNan());
+    const double ref = m == -INFINITY ? 0.0 : (double)m;
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) s += exp2_of(fmax((double)z[k] - ref, least), rate);
+    s = half_reduce(s, Add());
+    if (lane == 0) {
+      a.block_max[row * G + b] = m;
+      a.block_sum[row * G + b] = s;
+    }
   }
 }
 
@@ -246,7 +256,7 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
 //     before it give the cut (a few), or a radix search over their places in
 //     the order does (many).
 //  3. Where they are too many to list (top_p on a flat row), a histogram of
-//     about 32768 logits of the row tells near which value the cut lies; one
+//     about 16384 logits of the row tells near which value the cut lies; one
 //     pass adds up what is above that neighbourhood and lists what is in it.
 //  4. Where that fails too (a large k, thousands of equal logits at the cut),
 //     the neighbourhood is narrowed by exact histograms over places, 11 bits
@@ -265,7 +275,7 @@ constexpr int kBinsPer = kBins / NT;
 constexpr int kList = 4096;        // logits that can be listed
 constexpr int kRanked = NT / 4;    // up to so many, every listed logit is compared with every other
 constexpr int kDirect = 32;        // active blocks up to which top_p's candidates are listed without an estimate
-constexpr int kEstimate = 32768;   // logits of the estimate
+constexpr int kEstimate = 16384;   // logits of the estimate, at least
 constexpr int kAround = 1700;      // logits listed on either side of the estimated cut
 
 // A logit's place in the order, the larger the earlier: its key, then its
@@ -321,19 +331,22 @@ __device__ __forceinline__ void for_chunk(float (&z)[kChunk], F f) {
   }
 }
 
-struct Shared {
+struct Lists {  // for rows with limits only
   u64 list[kList];  // places
   u64 q[kList];     // their masses
   u64 mass[kBins];
   uint32_t count[kBins];
+};
+struct Shared {
   u64 scan64[kWaves];
   double scand[kWaves];
   uint32_t scan32[kWaves];
   float maxw[kWaves], minw[kWaves];
   int flag[kWaves];
+  float low;
   // what one thread found for all
   int block, bin, edge_lo, edge_hi;
-  uint32_t n, bin_count;
+  uint32_t n, few, bin_count;
   u64 place, a, b, bin_mass, above;
 };
 
@@ -341,48 +354,76 @@ template <typename T>
 struct RowSampler {
   const Row<T> r;
   Shared& sh;
+  Lists& ls;
   float* const bmax;    // [blocks] maxima
   u64* const bq;        // [blocks] the bits of the blocks' sums (doubles), later their kept masses
   uint16_t* const act;  // active blocks, by index
   const int nb;
   const float mf;
-  const double m, rate;
+  const double m, rate, least_d;
   double S, unit;       // sum of the weights; 2^F
   double least;         // min_p, or -1
 
-  __device__ __forceinline__ double weight(float z) const { return exp2_neg(((double)z - m) * rate); }
-  __device__ __forceinline__ u64 quant(double w) const { return (u64)rint(w * unit); }
+  // A logit of -inf weighs 2^-1000, which is nothing beside the largest's 1
+  // and a mass of 0.
+  __device__ __forceinline__ double weight(float z) const {
+    return exp2_of(fmax((double)z - m, least_d), rate);
+  }
+  // round(w 2^F), below 2^52: the low bits of the sum with 2^52
+  __device__ __forceinline__ u64 quant(double w) const {
+    return (u64)__double_as_longlong(fma(w, unit, 0x1p52)) & 0xfffffffffffffull;
+  }
   __device__ __forceinline__ float value_at(u64 place) const {
     return Key<T>::value((uint32_t)(place >> kIndexBits));
   }
 
-  // Of the values tried between lo and hi (each wave tries one, twice), the
-  // largest that at least k block maxima reach, or above which the blocks
-  // that reach it hold `goal` for certain; lo if none.
-  __device__ __forceinline__ float bound(float lo, float hi, bool by_count, int k, double goal) {
-#pragma unroll 1
-    for (int round = 0; round < 2; ++round) {
-      const float step = (hi - lo) / (kWaves + 1);
-      const int w = threadIdx.x >> 6;
-      const float x = lo + (float)(w + 1) * step;
-      const double wx = weight(x);
-      double s = 0.0;
-#pragma unroll 2
-      for (int b = threadIdx.x & 63; b < nb; b += 64) {
-        const double held = fmax(__longlong_as_double((long long)bq[b]) - kSampleBlock * wx, wx);
-        s += bmax[b] >= x ? (by_count ? 1.0 : held) : 0.0;
-      }
-      s = wave_reduce(s, Add());
-      if ((threadIdx.x & 63) == 0) sh.flag[w] = s >= (by_count ? (double)k : goal);
-      __syncthreads();
-      // f falls with x: the last wave that says yes
-      int n = 64 - __clzll((long long)__ballot((threadIdx.x & 63) < kWaves && sh.flag[threadIdx.x & (kWaves - 1)]));
-      __syncthreads();
-      n = uniform(n);
-      if (n < kWaves) hi = lo + (float)(n + 1) * step;
-      if (n > 0) lo = lo + (float)n * step;
+  // The highest of 2048 values between lowest_max and mf that at least k block
+  // maxima reach, or above which the blocks that reach it hold `goal` even if
+  // all their logits below it were as large as it; `none` if there is none. A
+  // histogram of the maxima, with the blocks' masses.
+  __device__ __forceinline__ float bound(float lowest_max, bool by_count, int k, double goal, float none) {
+    const float scale = (float)kBins / (mf - lowest_max);
+    if (threadIdx.x == 0) sh.bin = -1;
+    clear_bins();
+    for (int b = threadIdx.x; b < nb; b += NT) {
+      if (bmax[b] == -INFINITY) continue;
+      const int bin = max(0, min(kBins - 1, (int)((bmax[b] - lowest_max) * scale)));
+      atomicAdd(&ls.count[bin], 1u);
+      if (!by_count) atomicAdd(&ls.mass[bin], quant(__longlong_as_double((long long)bq[b])));
     }
-    return lo;
+    __syncthreads();
+    uint32_t c = 0, tc;
+    u64 q = 0, tq;
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
+      c += ls.count[bin], q += ls.mass[bin];
+    }
+    c = block_scan(c, sh.scan32, tc);
+    if (!by_count) q = block_scan(q, sh.scan64, tq);
+    // a hundredth of a bin lower, so that a bin's rounding does not matter
+    const auto value = [&](int bin) { return lowest_max + ((float)bin - 0.01f) / scale; };
+    int best = -1;  // bins fall with the thread: the first to say yes has the highest
+#pragma unroll
+    for (int i = 0; i < kBinsPer; ++i) {
+      const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
+      c += ls.count[bin], q += ls.mass[bin];
+      const bool yes = by_count ? (int)c >= k
+                                : c > 0 && (double)q >= goal + (double)c * kSampleBlock * weight(value(bin)) * unit;
+      if (yes && best < 0) best = bin;
+    }
+    const u64 said = __ballot(best >= 0);
+    if (said && (threadIdx.x & 63) == (unsigned)__ffsll(said) - 1) atomicMax(&sh.bin, best);
+    __syncthreads();
+    const int bin = uniform(sh.bin);
+    return bin < 0 ? none : value(bin);
+  }
+
+  // Whether a block holds a 32nd of the row's mass.
+  __device__ __forceinline__ bool peaked() {
+    bool yes = false;
+    for (int b = threadIdx.x; b < nb; b += NT) yes |= __longlong_as_double((long long)bq[b]) * 32.0 >= S;
+    return __syncthreads_or(yes ? 1 : 0) != 0;
   }
 
   // Lists the active blocks: those whose maximum is at least z.
@@ -397,14 +438,23 @@ struct RowSampler {
     return uniform((int)total);
   }
 
-  // Over the active blocks: the mass of the logits before hi in the order (in
-  // sh.above), into bq what of it min_p keeps, and into the list the places
-  // from hi to lo (sh.n of them; those past kList are only counted).
-  __device__ __forceinline__ void pass(int nact, u64 lo, u64 hi) {
-    constexpr int step = NT / kLanes;
+  __device__ __forceinline__ void begin_pass() {
     for (int b = threadIdx.x; b < nb; b += NT) bq[b] = 0;
     if (threadIdx.x == 0) sh.n = 0, sh.above = 0;
     __syncthreads();
+  }
+  __device__ __forceinline__ void end_pass(u64 above) {
+    above = wave_reduce(above, Add());
+    if ((threadIdx.x & 63) == 0 && above) atomicAdd(&sh.above, above);
+    __syncthreads();
+  }
+
+  // Over the active blocks: the mass of the logits at or above zh (in
+  // sh.above), into bq what of it min_p keeps, and into the list the places of
+  // those from zl on (sh.n of them; those past kList are only counted).
+  __device__ __forceinline__ void pass(int nact, float zl, float zh) {
+    constexpr int step = NT / kLanes;
+    begin_pass();
     u64 above = 0;
     const int lane = threadIdx.x % kLanes;
     float z[kChunk], next[kChunk];
@@ -416,44 +466,79 @@ struct RowSampler {
         r.load(bnext * kLanes + lane, next);
       }
       if (i >= 0) {
-        u64 kept = 0;
         uint32_t listed = 0;
-        const int e0 = r.first(b * kLanes + lane);
-        for_chunk(z, [&](int k, float x) {
-          const u64 place = place_of(Key<T>::of(x), e0 + k);
-          if (place > hi) {
-            const double w = weight(x);
-            const u64 q = quant(w);
-            above += q;
-            if (w >= least) kept += q;
-          } else if (place >= lo) {
-            listed |= 1u << k;
-          }
-        });
-        if (__ballot(kept != 0)) {
-          kept = half_reduce(kept, Add());
-          if (lane == 0) bq[b] = kept;
-        }
+#pragma unroll
+        for (int k = 0; k < kChunk; ++k) listed |= (z[k] >= zl) & (z[k] < zh) ? 1u << k : 0u;
         if (__ballot(listed != 0)) {  // one addition to the count a wave (a half at the end)
+          const int e0 = r.first(b * kLanes + lane);
           const uint32_t mine = (uint32_t)__popc(listed), upto = wave_scan(mine);
           const int last = 63 - __clzll((long long)__ballot(1));
           uint32_t at = 0;
           if ((int)(threadIdx.x & 63) == last) at = atomicAdd(&sh.n, upto);
           at = lane_of(at, last) + upto - mine;
-          for_chunk(z, [&](int k, float x) {
+#pragma unroll
+          for (int k = 0; k < kChunk; ++k)
             if (listed >> k & 1) {
-              if (at < kList) sh.list[at] = place_of(Key<T>::of(x), e0 + k);
+              if (at < kList) ls.list[at] = place_of(Key<T>::of(z[k]), e0 + k);
               ++at;
             }
-          });
+        }
+        if (zh < INFINITY) {  // uniform
+          // those not above as -inf, which has no mass: nothing depends on a
+          // branch, and the eight chains overlap
+          u64 kept = 0, all = 0;
+          if (least > 0.0) {
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k) {
+              const double w = weight(z[k] >= zh ? z[k] : -INFINITY);
+              const u64 q = quant(w);
+              all += q;
+              kept += w >= least ? q : 0;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k) all += quant(weight(z[k] >= zh ? z[k] : -INFINITY));
+            kept = all;
+          }
+          above += all;
+          kept = half_reduce(kept, Add());
+          if (lane == 0) bq[b] = kept;
         }
       }
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) z[k] = next[k];
       b = bnext;
     }
-    if (above) atomicAdd(&sh.above, above);
-    __syncthreads();
+    end_pass(above);
+  }
+
+  // The same over the whole row with bounds at places: above hi, and from hi
+  // to lo.
+  __device__ __forceinline__ void pass_places(u64 lo, u64 hi) {
+    begin_pass();
+    u64 above = 0;
+    const int lane = threadIdx.x % kLanes;
+#pragma unroll 1
+    for (int b = threadIdx.x / kLanes; b < nb; b += NT / kLanes) {
+      const int c = b * kLanes + lane, e0 = r.first(c);
+      float z[kChunk];
+      r.load(c, z);
+      u64 kept = 0;
+      for_chunk(z, [&](int k, float x) {
+        const u64 place = place_of(Key<T>::of(x), e0 + k);
+        if (place > hi) {
+          const double w = weight(x);
+          above += quant(w);
+          kept += w >= least ? quant(w) : 0;
+        } else if (place >= lo) {
+          const uint32_t at = atomicAdd(&sh.n, 1u);
+          if (at < kList) ls.list[at] = place;
+        }
+      });
+      kept = half_reduce(kept, Add());
+      if (lane == 0) bq[b] = kept;
+    }
+    end_pass(above);
   }
 
   // The least whole mass at or above p times `mass`, and at least 1.
@@ -462,47 +547,52 @@ struct RowSampler {
     return t < 1.0 ? 1ull : (u64)t;
   }
 
-  // The cut within the list of n, above which lies the mass `above`: kept are
+  // The cut within the list of n places from hi to lo, above which lies the
+  // mass `above`: kept are
   // the first k (k >= n: no limit) of those the mass before which is below p
   // times the mass of the first k with k_on, else of everything. False if the
   // cut is not in the list, unless `whole`: then all of it is kept. Adds the
   // kept ones to bq; through: the mass up to and with the cut.
-  __device__ __forceinline__ bool cut_in_list(int n, u64 above, u64 k, bool k_on, float p, double mass, bool whole,
-                                              u64& cut, u64& through) {
+  __device__ __forceinline__ bool cut_in_list(int n, u64 lo, u64 hi, u64 above, u64 k, bool k_on, float p, double mass,
+                                              bool whole, u64& cut, u64& through) {
     u64 mine = 0, total;
 #pragma unroll 1
     for (int j = threadIdx.x; j < n; j += NT) {
-      const u64 q = quant(weight(value_at(sh.list[j])));
-      sh.q[j] = q;
+      const u64 q = quant(weight(value_at(ls.list[j])));
+      ls.q[j] = q;
       mine += q;
     }
-    block_scan(mine, sh.scan64, total);
-    total = uniform(total);
     u64 t = ~0ull;
     if (n <= kRanked) {
       // every place against every other: four threads share one, each with a
       // quarter of the list
       const int e = threadIdx.x >> 2;
       const bool in = e < n;
-      const u64 place = in ? sh.list[e] : 0, q = in ? sh.q[e] : 0;
-      u64 rank = 0, before = 0;
+      __syncthreads();
+      const u64 place = in ? ls.list[e] : 0, q = in ? ls.q[e] : 0;
+      uint32_t rank = 0;
+      u64 before = 0;
       if (in)
 #pragma unroll 4
-        for (int j = threadIdx.x & 3; j < n; j += 4)
-          if (sh.list[j] > place) ++rank, before += sh.q[j];
-      rank += __shfl_xor(rank, 1, 64);
-      rank += __shfl_xor(rank, 2, 64);
-      before += __shfl_xor(before, 1, 64);
-      before += __shfl_xor(before, 2, 64);
+        for (int j = threadIdx.x & 3; j < n; j += 4) {
+          const bool first = ls.list[j] > place;
+          rank += first;
+          before += first ? ls.q[j] : 0;
+        }
+      rank += permuted<0xb1, 0xf>(rank);
+      rank += permuted<0x4e, 0xf>(rank);
+      before += permuted<0xb1, 0xf>(before);
+      before += permuted<0x4e, 0xf>(before);
       before += above;
       const bool one = in && (threadIdx.x & 3) == 0;
-      if (one && (rank == k - 1 || (k >= (u64)n && rank == (u64)n - 1))) sh.a = before + q;
+      if (one && (rank == k - 1 || (k >= (u64)n && rank == (uint32_t)n - 1))) sh.a = before + q;
+      if (one && rank == (uint32_t)n - 1) sh.bin_mass = before + q;
       __syncthreads();
       if (p < 1.f) {
         t = uniform(needed(p, k_on ? (double)sh.a : mass));
-        if (above >= t || (!whole && t > above + total)) return false;  // uniform
+        if (above >= t || (!whole && t > uniform(sh.bin_mass))) return false;  // uniform
       }
-      if (one && rank < k && before < t && (rank + 1 == (u64)n || rank + 1 >= k || before + q >= t)) {
+      if (one && rank < k && before < t && (rank + 1 == (uint32_t)n || rank + 1 >= k || before + q >= t)) {
         sh.place = place;
         sh.b = before + q;
       }
@@ -510,7 +600,9 @@ struct RowSampler {
       cut = uniform(sh.place);
       through = uniform(sh.b);
     } else {
-      u64 lo = 0;
+      block_scan(mine, sh.scan64, total);
+      total = uniform(total);
+      u64 at = lo;  // the earliest cut so far
       through = above + total;
 #pragma unroll 1
       for (int by_mass = 0; by_mass < 2; ++by_mass) {
@@ -524,24 +616,16 @@ struct RowSampler {
         } else if (k >= (u64)n) {
           continue;
         }
-        const u64 at = radix(by_mass, target, lo, got);
-        lo = at > lo ? at : lo;
+        at = radix(by_mass, target, at, hi, got);
         through = above + got;
       }
-      cut = lo;
-      if (lo == 0) {  // all of it: the last one's place
-        if (threadIdx.x == 0) sh.place = ~0ull;
-        __syncthreads();
-        for (int j = threadIdx.x; j < n; j += NT) atomicMin(&sh.place, sh.list[j]);
-        __syncthreads();
-        cut = uniform(sh.place);
-      }
+      cut = at;  // or lo, the last place there can be: all of it
     }
 #pragma unroll 1
     for (int j = threadIdx.x; j < n; j += NT) {
-      const u64 place = sh.list[j];
+      const u64 place = ls.list[j];
       if (place >= cut && (least <= 0.0 || weight(value_at(place)) >= least))
-        atomicAdd(&bq[(index_at(place) + r.lead) / kSampleBlock], sh.q[j]);
+        atomicAdd(&bq[(index_at(place) + r.lead) / kSampleBlock], ls.q[j]);
     }
     __syncthreads();
     return true;
@@ -557,23 +641,23 @@ struct RowSampler {
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
       const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
-      c0 += sh.count[bin], m0 += sh.mass[bin];
+      c0 += ls.count[bin], m0 += ls.mass[bin];
     }
-    // both sums in one scan: counts are below 2^20 and masses below 2^62, so
-    // each needs its own
-    c0 = an + block_scan(c0, sh.scan64, tc);
+    // by mass, the count above is not needed
+    tc = 0;
+    if (!by_mass) c0 = an + block_scan(c0, sh.scan64, tc);
     m0 = am + block_scan(m0, sh.scan64, tm);
     if (uniform(target > (by_mass ? am + tm : an + tc) ? 1 : 0)) return false;
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
       const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
-      const u64 c1 = c0 + sh.count[bin], m1 = m0 + sh.mass[bin];
+      const u64 c1 = c0 + ls.count[bin], m1 = m0 + ls.mass[bin];
       if ((by_mass ? m0 : c0) < target && (by_mass ? m1 : c1) >= target) {  // one thread, one bin
         sh.bin = bin;
         sh.a = c0;
         sh.b = m0;
-        sh.bin_count = sh.count[bin];
-        sh.bin_mass = sh.mass[bin];
+        sh.bin_count = ls.count[bin];
+        sh.bin_mass = ls.mass[bin];
       }
       c0 = c1;
       m0 = m1;
@@ -588,7 +672,7 @@ struct RowSampler {
   }
 
   __device__ __forceinline__ void clear_bins() {
-    for (int i = threadIdx.x; i < kBins; i += NT) sh.mass[i] = 0, sh.count[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += NT) ls.mass[i] = 0, ls.count[i] = 0;
     __syncthreads();
   }
   static __device__ __forceinline__ int shift_of(u64 range) {
@@ -596,10 +680,10 @@ struct RowSampler {
     return bits > 11 ? bits - 11 : 0;
   }
 
-  // Among the listed places at or above `least_place` the one at which
-  // `target` is first reached, which it is; through: the mass up to and with it.
-  __device__ __forceinline__ u64 radix(bool by_mass, u64 target, u64 least_place, u64& through) {
-    u64 lo = least_place, hi = last_place(Key<T>::of(mf)) | kIndexMask, am = 0, an = 0;
+  // Among the listed places from hi to lo the one at which `target` is first
+  // reached, which it is; through: the mass up to and with it.
+  __device__ __forceinline__ u64 radix(bool by_mass, u64 target, u64 lo, u64 hi, u64& through) {
+    u64 am = 0, an = 0;
     const int n = uniform((int)sh.n);
 #pragma unroll 1
     for (;;) {
@@ -607,23 +691,44 @@ struct RowSampler {
       clear_bins();
 #pragma unroll 1
       for (int j = threadIdx.x; j < n; j += NT) {
-        const u64 place = sh.list[j];
+        const u64 place = ls.list[j];
         if (place >= lo && place <= hi) {
-          atomicAdd(&sh.mass[(place - lo) >> shift], sh.q[j]);
-          atomicAdd(&sh.count[(place - lo) >> shift], 1u);
+          atomicAdd(&ls.mass[(place - lo) >> shift], ls.q[j]);
+          atomicAdd(&ls.count[(place - lo) >> shift], 1u);
         }
       }
       __syncthreads();
       if (!step(by_mass, target, lo, hi, shift, am, an)) break;
       const int left = uniform((int)sh.bin_count);
-      through = am + uniform(sh.bin_mass);
+      if (threadIdx.x == 0) sh.few = 0;
       __syncthreads();
-      if (left == 1 || !shift) break;
+      if (left <= 64 || !shift) break;
     }
+    // the few that are left, each against the others
 #pragma unroll 1
-    for (int j = threadIdx.x; j < n; j += NT)
-      if (sh.list[j] >= lo && sh.list[j] <= hi) sh.place = sh.list[j];
+    for (int j = threadIdx.x; j < n; j += NT) {
+      const u64 place = ls.list[j];
+      if (place >= lo && place <= hi) {
+        const uint32_t at = atomicAdd(&sh.few, 1u);
+        ls.mass[at] = place;
+        ls.mass[64 + at] = ls.q[j];
+      }
+    }
     __syncthreads();
+    const int few = uniform((int)sh.few);
+    if ((int)threadIdx.x < few) {
+      const u64 place = ls.mass[threadIdx.x], q = ls.mass[64 + threadIdx.x];
+      u64 before = by_mass ? am : an, mass = am;
+      for (int j = 0; j < few; ++j)
+        if (ls.mass[j] > place) {
+          const u64 qj = ls.mass[64 + j];
+          before += by_mass ? qj : 1;
+          mass += qj;
+        }
+      if (before < target && before + (by_mass ? q : 1) >= target) sh.place = place, sh.b = mass + q;
+    }
+    __syncthreads();
+    through = uniform(sh.b);
     return uniform(sh.place);
   }
 
@@ -646,8 +751,8 @@ struct RowSampler {
         for_chunk(z, [&](int k, float x) {
           const u64 place = place_of(Key<T>::of(x), e0 + k);
           if (place >= lo && place <= hi) {
-            atomicAdd(&sh.mass[(place - lo) >> shift], quant(weight(x)));
-            atomicAdd(&sh.count[(place - lo) >> shift], 1u);
+            atomicAdd(&ls.mass[(place - lo) >> shift], quant(weight(x)));
+            atomicAdd(&ls.count[(place - lo) >> shift], 1u);
           }
         });
       }
@@ -664,14 +769,15 @@ struct RowSampler {
     }
   }
 
-  // Bounds of a neighbourhood of the cut, above which a mass of `t` of the
-  // row's lies, from a sample of the row in which the mass below the cut is
+  // Bounds zl (raised) and zh of a neighbourhood of the cut, above which a mass
+  // of `t` of the row's lies, from a sample of the row in which the mass below the cut is
   // counted from the bottom, where no single logit weighs much. Logits below
   // zl are surely below the cut.
-  __device__ __forceinline__ void estimate(u64 t, float zl, u64& lo, u64& hi) {
+  __device__ __forceinline__ void estimate(u64 t, float& zl, float& zh) {
     const float scale = (float)kBins / (mf - zl), ratef = (float)rate;
     const int chunks = r.chunks(), step = max(1, chunks * kChunk / kEstimate);
-    if (threadIdx.x == 0) sh.bin = kBins - 1, sh.bin_count = 0, sh.edge_lo = 0, sh.edge_hi = kBins;
+    const float rest = 1.f / scale;
+    if (threadIdx.x == 0) sh.bin = kBins - 1, sh.bin_count = 0, sh.edge_lo = 0, sh.edge_hi = kBins, sh.low = 0.f;
     clear_bins();
     float low = 0.f;
 #pragma unroll 1
@@ -681,41 +787,54 @@ struct RowSampler {
 #pragma unroll
       for (int k = 0; k < kChunk; ++k)
         if (z[k] >= zl)
-          atomicAdd(&sh.count[min(kBins - 1, (int)((z[k] - zl) * scale))], 1u);
+          atomicAdd(&ls.count[min(kBins - 1, (int)((z[k] - zl) * scale))], 1u);
         else
-          low += exp2f((z[k] - mf) * ratef);
+          low += __builtin_amdgcn_exp2f((z[k] - mf) * ratef);
     }
+    // in any order: the estimate only says where to look
+    low = wave_reduce(low, Add());
+    if ((threadIdx.x & 63) == 0 && low > 0.f) atomicAdd(&sh.low, low);
     __syncthreads();
-    double mass[kBinsPer], mine = 0.0, all, lows;
-    uint32_t cnt[kBinsPer], n = 0, total;
+    double mass[kBinsPer];
+    uint32_t cnt[kBinsPer];
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
       const int bin = threadIdx.x * kBinsPer + i;
-      cnt[i] = sh.count[bin];
-      mass[i] = (double)cnt[i] * (double)exp2f((zl + ((float)bin + 0.5f) / scale - mf) * ratef);
-      mine += mass[i];
-      n += cnt[i];
+      cnt[i] = ls.count[bin];
+      mass[i] = (double)cnt[i] * (double)__builtin_amdgcn_exp2f((zl + ((float)bin + 0.5f) * rest - mf) * ratef);
     }
-    block_scan((double)low, sh.scand, lows);
-    double run = block_scan(mine, sh.scand, all);
-    const uint32_t c0 = block_scan(n, sh.scan32, total);
+    // counts and masses in one scan: the count in the low 20 bits, the mass
+    // above them in units that make the mass sought 2^30 of them, a bin's at
+    // most 2^32
+    const double lows = (double)sh.low;
     const double below = (S - (double)t / unit) / step - lows;  // of the sample, from zl on
-    uint32_t at = c0;
+    const double fine = 0x1p30 / fmax(below, 1e-300);
+    u64 both[kBinsPer], mine = 0, all;
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
-      if (run < below && run + mass[i] >= below) {
-        sh.bin = threadIdx.x * kBinsPer + i;
-        sh.bin_count = at;
-      }
-      run += mass[i];
-      at += cnt[i];
+      both[i] = (u64)fmin(mass[i] * fine, 0x1p32) << 20 | cnt[i];
+      mine += both[i];
     }
-    if (threadIdx.x == 0 && below <= 0.0) sh.bin = 0;
-    if (threadIdx.x == 0 && below > all) sh.bin_count = total;
+    u64 run = block_scan(mine, sh.scan64, all);
+    const uint32_t c0 = (uint32_t)run & 0xfffff;
+    if (below > 0.0) {
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        if ((run >> 20) < 1u << 30 && ((run + both[i]) >> 20) >= 1u << 30) {
+          sh.bin = threadIdx.x * kBinsPer + i;
+          sh.bin_count = (uint32_t)run & 0xfffff;
+        }
+        run += both[i];
+      }
+    } else if (threadIdx.x == 0) {
+      sh.bin = 0;
+    }
+    if (threadIdx.x == 0 && (all >> 20) < 1u << 30) sh.bin_count = (uint32_t)all & 0xfffff;
+    uint32_t at;
     __syncthreads();
     // edges: kAround logits below the cut's bin and above it
     const int around = kAround / step;
-    const int lo_at = (int)sh.bin_count - around, hi_at = (int)(sh.bin_count + sh.count[sh.bin]) + around;
+    const int lo_at = (int)sh.bin_count - around, hi_at = (int)(sh.bin_count + ls.count[sh.bin]) + around;
     at = c0;
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
@@ -726,8 +845,8 @@ struct RowSampler {
     }
     __syncthreads();
     const int edge_lo = uniform(sh.edge_lo), edge_hi = uniform(sh.edge_hi);
-    if (edge_lo > 0) lo = last_place(Key<T>::of(zl + (float)edge_lo / scale));
-    if (edge_hi < kBins) hi = last_place(Key<T>::of(zl + (float)edge_hi / scale)) - 1;
+    if (edge_hi < kBins) zh = zl + (float)edge_hi / scale;
+    if (edge_lo > 0) zl += (float)edge_lo / scale;
   }
 
   // The cut's place, and the blocks' kept masses in bq, which holds the
@@ -736,14 +855,17 @@ struct RowSampler {
     const bool k_on = top_k > 0 && top_k < r.V, p_on = top_p < 1.f;
     const uint32_t lowest = Key<T>::of(-INFINITY) + 1;  // the least finite key
     const float all = Key<T>::value(lowest);
-    float L = all, from = lowest_max;
+    float L = all, from = all;
     double goal = 0.0;
     if (!k_on && p_on) {
-      goal = (double)top_p * S * (1.0 + 1e-9);
+      goal = (double)top_p * S * unit * (1.0 + 1e-9);
       // with every other logit at most (1 - p) S / (2 x their number), it holds
       from = fmaxf(all, (float)(m + log2((1.0 - (double)fmaxf(top_p, 0.f)) * S / (512.0 * nb)) / rate));
     }
-    if (k_on ? top_k <= nb : p_on) L = bound(from, mf, k_on, top_k, goal);
+    // (a row none of whose blocks holds a 32nd is flat: the bound would not be far above `from`)
+    const bool flat = !k_on && p_on && !peaked();
+    if (flat) L = from;
+    else if (k_on ? top_k <= nb : p_on) L = bound(lowest_max, k_on, top_k, goal, k_on ? all : from);
     bool whole = false;  // whether what lies below L is cut by min_p, whatever the mass above it
     if (!k_on && least > 0.0) {
       const double z = m + (log2(least) - 1e-6) / rate;  // below it, w < min_p for certain
@@ -753,9 +875,10 @@ struct RowSampler {
       whole = zm >= L;
       L = fmaxf(L, zm);
     }
-    L = uniform(L);
+    L = fmaxf(uniform(L), all);
     int nact = activate(L);
     if (k_on && nact < top_k) nact = activate(L = all);  // fewer blocks than k, or than k that hold anything
+    const u64 top = last_place(Key<T>::of(mf)) | kIndexMask;
     u64 place = last_place(lowest), through = 0;
     double mass = S * unit;
     u64 k = k_on ? (u64)top_k : ~0ull;
@@ -765,31 +888,34 @@ struct RowSampler {
 #pragma unroll 1
     for (int method = k_on || !limits || nact <= kDirect || !(L < mf) ? 0 : 1; method < 3; ++method) {
       if (method == 1 && (k_on || !(L < mf))) continue;
-      if (method == 2) nact = activate(all);
-      const u64 bottom = last_place(max(lowest, Key<T>::of(method == 2 ? all : L)));
-      u64 lo = bottom, hi = last_place(Key<T>::of(mf)) | kIndexMask;
-      u64 an = 0;
-      if (!limits) hi = lo - 1;
-      if (method == 1) estimate(needed(top_p, mass), L, lo, hi);
-      const bool one_limit = method == 2 && count && p_on;  // k's cut first, then top_p's
-      if (method == 2) narrow(!count, count ? k : needed(top_p, mass), lo, hi, an);
-      pass(nact, lo, hi);
+      u64 lo = place, hi = top, an = 0;
+      bool one_limit = false;  // k's cut first, then top_p's
+      if (method < 2) {
+        float zl = L, zh = limits ? INFINITY : L;
+        if (method == 1) estimate(needed(top_p, mass), zl, zh);
+        pass(nact, zl, zh);
+        if (!limits) return place;
+        lo = last_place(max(lowest, Key<T>::of(zl)));  // at or below every place listed
+        whole = whole && zl == L;
+      } else {
+        whole = false;
+        lo = last_place(lowest);
+        one_limit = count && p_on;
+        narrow(!count, count ? k : needed(top_p, mass), lo, hi, an);
+        pass_places(lo, hi);
+      }
       const int n = uniform((int)sh.n);
       const u64 above = uniform(sh.above);
-      if (!limits) return place;
       if (method == 2 && hi < lo) {  // never reached: everything
+        if (!one_limit) return lo;
+        through = above;
+      } else {
+        if (n == 0 || n > kList) continue;
+        if (!cut_in_list(n, lo, hi, above, k == ~0ull ? k : k - an, count, one_limit ? 1.f : top_p, mass, whole, place,
+                         through))
+          continue;
         if (!one_limit) return place;
-        mass = (double)above;
-        count = false;
-        method = 1;
-        k = ~0ull;
-        continue;
       }
-      if (n == 0 || n > kList) continue;
-      if (!cut_in_list(n, above, k == ~0ull ? k : k - an, count, one_limit ? 1.f : top_p, mass, whole && lo == bottom, place,
-                       through))
-        continue;
-      if (!one_limit) return place;
       mass = (double)through;
       count = false;
       method = 1;
@@ -799,13 +925,19 @@ struct RowSampler {
   }
 };
 
-template <typename T>
+// Bytes of LDS before the lists.
+__host__ __device__ inline size_t shared_bytes(int G) {
+  return (sizeof(Shared) + (size_t)G * (sizeof(u64) + sizeof(float) + sizeof(uint16_t)) + 15) / 16 * 16;
+}
+
+template <typename T, bool LIMITS>  // whether there may be any
 __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
   extern __shared__ char lds[];
   Shared& sh = *reinterpret_cast<Shared*>(lds);
   u64* bq = reinterpret_cast<u64*>(lds + sizeof(Shared));
   float* bmax = reinterpret_cast<float*>(bq + G);
   uint16_t* act = reinterpret_cast<uint16_t*>(bmax + G);
+  Lists& ls = *reinterpret_cast<Lists*>(lds + shared_bytes(G));
   const int64_t row = blockIdx.x;
   const Row<T> r(a, row);
   const int nb = r.blocks();
@@ -868,7 +1000,8 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
     return;
   }
 
-  RowSampler<T> s{r, sh, bmax, bq, act, nb, mf, uniform((double)mf), uniform(rate_of(tau)), 0.0, 0.0,
+  RowSampler<T> s{r, sh, ls, bmax, bq, act, nb, mf, uniform((double)mf), uniform(rate_of(tau)),
+                  uniform(least_of(tau)), 0.0, 0.0,
                   uniform(min_p > 0.f ? fmin((double)min_p, 1.0) : -1.0)};
   const int per = (nb + NT - 1) / NT;  // blocks a thread takes, one after the other
   const int b0 = min(nb, (int)threadIdx.x * per), b1 = min(nb, b0 + per);
@@ -881,11 +1014,11 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
   }
   block_scan(sum, sh.scand, s.S);
   s.S = uniform(s.S);
-  // q = round(w 2^F) add up to less than 2^62: S < 2^(e+1), and the roundings
+  // q = round(w 2^F) add up to less than 2^52: S < 2^(e+1), and the roundings
   // add at most half of V <= 2^20
-  s.unit = uniform(ldexp(1.0, 60 - ilogb(s.S)));
+  s.unit = uniform(ldexp(1.0, 50 - ilogb(s.S)));
   u64 cut = 0;
-  const bool limited = (top_k > 0 && top_k < a.V) || top_p < 1.f || min_p > 0.f;
+  const bool limited = LIMITS && ((top_k > 0 && top_k < a.V) || top_p < 1.f || min_p > 0.f);
   if (limited) cut = s.cut(top_k, top_p, lowest_max);
   u64 mine = 0, total;
 #pragma unroll 1
@@ -931,7 +1064,6 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
 template <typename T>
 hipError_t sample(const SampleArgs& a, hipStream_t st) {
   const int G = sample_blocks(a.V);
-  const size_t lds = sizeof(Shared) + (size_t)G * (sizeof(u64) + sizeof(float) + sizeof(uint16_t));
   for (int64_t r0 = 0; r0 < a.N; r0 += 32768) {  // the grid's second dimension holds 65535
     SampleArgs b = a;
     b.N = std::min<int64_t>(32768, a.N - r0);
@@ -946,9 +1078,15 @@ hipError_t sample(const SampleArgs& a, hipStream_t st) {
     if (a.kept_logp) b.kept_logp = a.kept_logp + r0;
     b.block_max = a.block_max + r0 * G;
     b.block_sum = a.block_sum + r0 * G;
-    sample_stats_kernel<T><<<dim3((G + kStatBlocks - 1) / kStatBlocks, (unsigned)b.N), kStatThreads, 0, st>>>(b, G);
+    // several blocks a half wave once that leaves enough workgroups for the chip
+    const int rounds = (int)std::max<int64_t>(1, std::min<int64_t>(4, b.N * G / (kStatBlocks * 2048)));
+    sample_stats_kernel<T><<<dim3((G + kStatBlocks * rounds - 1) / (kStatBlocks * rounds), (unsigned)b.N), kStatThreads,
+                             0, st>>>(b, G, rounds);
     if (hipError_t e = hipGetLastError()) return e;
-    sample_row_kernel<T><<<(unsigned)b.N, NT, lds, st>>>(b, G);
+    if (a.top_k_rows || a.top_p_rows || a.min_p_rows || (a.top_k > 0 && a.top_k < a.V) || a.top_p < 1.f || a.min_p > 0.f)
+      sample_row_kernel<T, true><<<(unsigned)b.N, NT, shared_bytes(G) + sizeof(Lists), st>>>(b, G);
+    else
+      sample_row_kernel<T, false><<<(unsigned)b.N, NT, shared_bytes(G), st>>>(b, G);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
