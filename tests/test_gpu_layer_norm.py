@@ -13,6 +13,14 @@ from tests.gpu_helpers import require_gpu
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def float32_default():
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
 U = 2.0 ** -24
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 

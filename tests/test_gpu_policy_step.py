@@ -11,6 +11,14 @@ from tests.gpu_helpers import require_gpu
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def float32_default():
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 def setup(dtype, B=4, T=24, H=128, V=700, seed=0):
     g = torch.Generator().manual_seed(seed)
     t = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).to(dtype).cuda()  # noqa: E731
