@@ -255,9 +255,10 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
 //  2. The logits at or above it are listed in LDS; each one's rank and the mass
 //     before it give the cut (a few), or a radix search over their places in
 //     the order does (many).
-//  3. Where they are too many to list (top_p on a flat row), a histogram of
-//     about 16384 logits of the row tells near which value the cut lies; one
-//     pass adds up what is above that neighbourhood and lists what is in it.
+//  3. Where the maxima give no bound (fewer blocks than k) or the candidates
+//     are too many to list (top_p on a flat row), a histogram of about 16384
+//     logits of the row tells near which value the cut lies; one pass adds up
+//     what is above that neighbourhood and lists what is in it.
 //  4. Where that fails too (a large k, thousands of equal logits at the cut),
 //     the neighbourhood is narrowed by exact histograms over places, 11 bits
 //     a pass, until it can be listed.
@@ -274,6 +275,7 @@ constexpr int kBins = 2048;
 constexpr int kBinsPer = kBins / NT;
 constexpr int kList = 4096;        // logits that can be listed
 constexpr int kRanked = NT / 4;    // up to so many, every listed logit is compared with every other
+constexpr int kAll = 1536;         // logits up to which a whole row is listed for top_k
 constexpr int kDirect = 32;        // active blocks up to which top_p's candidates are listed without an estimate
 constexpr int kEstimate = 16384;   // logits of the estimate, at least
 constexpr int kAround = 1700;      // logits listed on either side of the estimated cut
@@ -769,11 +771,12 @@ struct RowSampler {
     }
   }
 
-  // Bounds zl (raised) and zh of a neighbourhood of the cut, above which a mass
-  // of `t` of the row's lies, from a sample of the row in which the mass below the cut is
+  // Bounds zl (raised) and zh of a neighbourhood of the cut. By count: a zl
+  // that k logits surely reach, give or take four standard deviations of the
+  // sample. Else of the cut above which a mass of `t` of the row's lies, from a sample of the row in which the mass below the cut is
   // counted from the bottom, where no single logit weighs much. Logits below
   // zl are surely below the cut.
-  __device__ __forceinline__ void estimate(u64 t, float& zl, float& zh) {
+  __device__ __forceinline__ void estimate(bool by_count, u64 t, float& zl, float& zh) {
     const float scale = (float)kBins / (mf - zl), ratef = (float)rate;
     const int chunks = r.chunks(), step = max(1, chunks * kChunk / kEstimate);
     const float rest = 1.f / scale;
@@ -817,6 +820,18 @@ struct RowSampler {
     }
     u64 run = block_scan(mine, sh.scan64, all);
     const uint32_t c0 = (uint32_t)run & 0xfffff;
+    if (by_count) {
+      const float aim = ((float)t + (step > 1 ? 4.f * sqrtf((float)t * (float)step) : 0.f)) / (float)step;
+      float left = (float)(((uint32_t)all & 0xfffff) - c0);
+#pragma unroll
+      for (int i = 0; i < kBinsPer; ++i) {
+        if (left >= aim && left - (float)cnt[i] < aim) sh.edge_lo = threadIdx.x * kBinsPer + i;
+        left -= (float)cnt[i];
+      }
+      __syncthreads();
+      zl += (float)uniform(sh.edge_lo) * rest;
+      return;
+    }
     if (below > 0.0) {
 #pragma unroll
       for (int i = 0; i < kBinsPer; ++i) {
@@ -877,7 +892,11 @@ struct RowSampler {
     }
     L = fmaxf(uniform(L), all);
     int nact = activate(L);
-    if (k_on && nact < top_k) nact = activate(L = all);  // fewer blocks than k, or than k that hold anything
+    bool known = !k_on || nact >= top_k;  // a bound for k from the maxima alone
+    if (!known && r.V <= kAll) {
+      nact = activate(L = all);
+      known = true;
+    }
     const u64 top = last_place(Key<T>::of(mf)) | kIndexMask;
     u64 place = last_place(lowest), through = 0;
     double mass = S * unit;
@@ -886,13 +905,17 @@ struct RowSampler {
     const bool limits = k_on || p_on;
     // 0: list all candidates; 1: those around an estimate of the cut; 2: narrow
 #pragma unroll 1
-    for (int method = k_on || !limits || nact <= kDirect || !(L < mf) ? 0 : 1; method < 3; ++method) {
-      if (method == 1 && (k_on || !(L < mf))) continue;
+    for (int method = known && (k_on || !limits || nact <= kDirect || !(L < mf)) ? 0 : 1; method < 3; ++method) {
+      if (method == 1 && (k_on ? top_k > kList / 2 : !(L < mf))) continue;
       u64 lo = place, hi = top, an = 0;
       bool one_limit = false;  // k's cut first, then top_p's
       if (method < 2) {
         float zl = L, zh = limits ? INFINITY : L;
-        if (method == 1) estimate(needed(top_p, mass), zl, zh);
+        if (method == 1) {
+          if (k_on) zl = fmaxf(all, lowest_max - 3.f * (mf - lowest_max));  // where the sample's histogram begins
+          estimate(k_on, k_on ? k : needed(top_p, mass), zl, zh);
+          if (k_on) nact = activate(zl);
+        }
         pass(nact, zl, zh);
         if (!limits) return place;
         lo = last_place(max(lowest, Key<T>::of(zl)));  // at or below every place listed
@@ -910,7 +933,7 @@ struct RowSampler {
         if (!one_limit) return lo;
         through = above;
       } else {
-        if (n == 0 || n > kList) continue;
+        if (n == 0 || n > kList || (method == 1 && k_on && n < top_k)) continue;
         if (!cut_in_list(n, lo, hi, above, k == ~0ull ? k : k - an, count, one_limit ? 1.f : top_p, mass, whole, place,
                          through))
           continue;
