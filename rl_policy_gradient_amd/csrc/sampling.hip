@@ -278,7 +278,7 @@ constexpr int kRanked = NT / 4;    // up to so many, every listed logit is compa
 constexpr int kAll = 1536;         // logits up to which a whole row is listed for top_k
 constexpr int kDirect = 32;        // active blocks up to which top_p's candidates are listed without an estimate
 constexpr int kEstimate = 16384;   // logits of the estimate, at least
-constexpr int kAround = 1700;      // logits listed on either side of the estimated cut
+constexpr int kAround = 1250;      // logits listed on either side of the estimated cut, three times its usual error
 
 // A logit's place in the order, the larger the earlier: its key, then its
 // index from the end.
