@@ -20,7 +20,6 @@ namespace plp {
 
 namespace {
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int NT = 256;
@@ -68,61 +67,58 @@ __device__ __forceinline__ Updated update(float p, float g, float m, float v, fl
 }
 
 // Four consecutive elements i .. i+3 of an array of n, those at or past n as
-// 0. `wide`: the array is 16-byte aligned (i is a multiple of 4).
-__device__ __forceinline__ f32x4 load4(const float* p, int64_t i, int64_t n, bool wide) {
-  if (wide && i + 4 <= n) return *reinterpret_cast<const f32x4*>(p + i);
-  f32x4 x;
+// 0. One load or store whatever the array's alignment: global memory asks
+// only for that of the elements.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+  typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <>
+struct Four<__bf16> {
+  typedef __bf16 raw __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Four<uint8_t> {
+  typedef uint8_t raw __attribute__((ext_vector_type(4), aligned(1)));
+};
+template <typename T>
+__device__ __forceinline__ typename Four<T>::raw load4(const T* p, int64_t i, int64_t n) {
+  typedef typename Four<T>::raw raw;
+  if (i + 4 <= n) return *reinterpret_cast<const raw*>(p + i);
+  raw x = {};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = i + k < n ? p[i + k] : 0.f;
+  for (int k = 0; k < 3; ++k)
+    if (i + k < n) x[k] = p[i + k];
   return x;
 }
-__device__ __forceinline__ f32x4 load4(const __bf16* p, int64_t i, int64_t n, bool wide) {
-  if (wide && i + 4 <= n) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p + i);
-    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                 __uint_as_float(u.y & 0xffff0000u)};
-  }
-  f32x4 x;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = i + k < n ? (float)p[i + k] : 0.f;
-  return x;
-}
-__device__ __forceinline__ uint32_t load4(const uint8_t* p, int64_t i, int64_t n, bool wide) {
-  if (wide && i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
-  uint32_t x = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x |= i + k < n ? (uint32_t)p[i + k] << 8 * k : 0u;
-  return x;
-}
-__device__ __forceinline__ void store4(float* p, int64_t i, int64_t n, bool wide, f32x4 x) {
-  if (wide && i + 4 <= n) {
-    *reinterpret_cast<f32x4*>(p + i) = x;
+template <typename T>
+__device__ __forceinline__ void store4(T* p, int64_t i, int64_t n, typename Four<T>::raw x) {
+  if (i + 4 <= n) {
+    *reinterpret_cast<typename Four<T>::raw*>(p + i) = x;
     return;
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < 3; ++k)
     if (i + k < n) p[i + k] = x[k];
 }
-__device__ __forceinline__ void store4(__bf16* p, int64_t i, int64_t n, bool wide, f32x4 x) {
-  bf16x4 y;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] = (__bf16)x[k];
-  if (wide && i + 4 <= n) {
-    *reinterpret_cast<bf16x4*>(p + i) = y;
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (i + k < n) p[i + k] = y[k];
+template <typename T>
+__device__ __forceinline__ f32x4 load4f(const T* p, int64_t i, int64_t n) {
+  return __builtin_convertvector(load4(p, i, n), f32x4);
 }
-__device__ __forceinline__ void store4(uint8_t* p, int64_t i, int64_t n, bool wide, uint32_t x) {
-  if (wide && i + 4 <= n) {
-    *reinterpret_cast<uint32_t*>(p + i) = x;
-    return;
-  }
+template <typename T>
+__device__ __forceinline__ void store4f(T* p, int64_t i, int64_t n, f32x4 x) {
+  typename Four<T>::raw y;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (i + k < n) p[i + k] = (uint8_t)(x >> 8 * k);
+  for (int k = 0; k < 4; ++k) y[k] = (T)x[k];
+  store4(p, i, n, y);
+}
+__device__ __forceinline__ uint32_t load_codes(const void* p, int64_t i, int64_t n) {
+  return __builtin_bit_cast(uint32_t, load4((const uint8_t*)p, i, n));
+}
+__device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t n, uint32_t c) {
+  store4((uint8_t*)p, i, n, __builtin_bit_cast(Four<uint8_t>::raw, c));
 }
 
 __device__ __forceinline__ f32x4 from_e4m3(uint32_t c) {
@@ -198,22 +194,21 @@ static_assert(kAdamBlock == 4 * 64 && kAdamTile == 4 * NT, "one block of a scale
 template <typename P, typename G, bool MASTER, bool BITS8>
 __device__ __forceinline__ void tile(const AdamTensor& t, const Scalars& s, float keep, int64_t begin) {
   const int64_t n = t.n, i = begin + threadIdx.x * 4, b = i / kAdamBlock;
-  const bool wide = t.wide;
   f32x4 p, g, m, v, r;
   if (MASTER)
-    p = load4((const float*)t.master, i, n, wide);
+    p = load4f((const float*)t.master, i, n);
   else
-    p = load4((const P*)t.param, i, n, wide);
-  g = load4((const G*)t.grad, i, n, wide);
+    p = load4f((const P*)t.param, i, n);
+  g = load4f((const G*)t.grad, i, n);
   if (BITS8) {
-    const uint32_t mc = load4((const uint8_t*)t.m, i, n, wide), vc = load4((const uint8_t*)t.v, i, n, wide);
+    const uint32_t mc = load_codes(t.m, i, n), vc = load_codes(t.v, i, n);
     const float ms = i < n ? t.ms[b] : 0.f, vs = i < n ? t.vs[b] : 0.f;
     m = from_e4m3(mc) * ms;
     r = from_e4m3(vc) * vs;
     v = r * r;
   } else {
-    m = load4((const float*)t.m, i, n, wide);
-    v = load4((const float*)t.v, i, n, wide);
+    m = load4f((const float*)t.m, i, n);
+    v = load4f((const float*)t.v, i, n);
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -223,19 +218,19 @@ __device__ __forceinline__ void tile(const AdamTensor& t, const Scalars& s, floa
     v[k] = x.v;
     r[k] = x.r;
   }
-  if (MASTER) store4(t.master, i, n, wide, p);
-  store4((P*)t.param, i, n, wide, p);
+  if (MASTER) store4f(t.master, i, n, p);
+  store4f((P*)t.param, i, n, p);
   if (BITS8) {  // elements past the end are all zero and do not count
     const Scale sm = scale_of(wave_max(finite_max(m))), sr = scale_of(wave_max(finite_max(r)));
-    store4((uint8_t*)t.m, i, n, wide, encode(m, sm, false));
-    store4((uint8_t*)t.v, i, n, wide, encode(r, sr, true));
+    store_codes(t.m, i, n, encode(m, sm, false));
+    store_codes(t.v, i, n, encode(r, sr, true));
     if ((threadIdx.x & 63) == 0 && i < n) {
       t.ms[b] = sm.s;
       t.vs[b] = sr.s;
     }
   } else {
-    store4((float*)t.m, i, n, wide, m);
-    store4((float*)t.v, i, n, wide, v);
+    store4f((float*)t.m, i, n, m);
+    store4f((float*)t.v, i, n, v);
   }
 }
 

@@ -38,10 +38,12 @@ __device__ float block_sum(float v, float* red) {
 
 // ---------------------------------------------------------------------------
 // Rows of up to 16384: the row stays in registers, 16 elements a lane, and
-// LPR = 8 .. 1024 lanes (the least power of two that holds it) share a row, so
-// a workgroup of 256 takes 256 / LPR rows at a time and short rows leave no
-// lane idle. V elements are loaded at once: 16 bytes where every array is
-// aligned and H a multiple of that, else one.
+// LPR lanes share a row: 8 .. 128, powers of two, in a workgroup of 256 that
+// takes 256 / LPR rows at a time, or a workgroup of 192 .. 1024 a row (the
+// least that hold it), so that no row leaves many lanes idle. A lane loads 16 bytes at a time, whatever the row's alignment
+// (global loads and stores need only that of their elements); the row's last
+// few elements are the end of its last 16 bytes, and are stored 8, 4 and 2
+// bytes at a time.
 // ---------------------------------------------------------------------------
 constexpr int kPerLane = 16;
 constexpr int kMaxLanes = 1024;
@@ -73,43 +75,86 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-// The 16 elements of a lane: V consecutive ones, then V more LPR V further on.
-// Those at or past H are 0.
-template <typename T, int V, int LPR>
-__device__ __forceinline__ void load_row(const T* p, int lane, int H, float (&x)[kPerLane]) {
-  typedef T TV __attribute__((ext_vector_type(V)));
+typedef unsigned __int128 Bits;
+// 16 bytes of T at any element's address.
+template <typename T>
+constexpr int vec_of = 16 / (int)sizeof(T);
+template <typename T>
+struct Vec {
+  typedef T type __attribute__((ext_vector_type(vec_of<T>), aligned(sizeof(T))));
+};
+
+// The 16 elements of a lane as they lie in memory: V consecutive ones, then V
+// more LPR V further on. Those at or past H are 0. TAIL: H is no multiple of V.
+template <typename T>
+struct Raw {
+  static constexpr int V = vec_of<T>, C = kPerLane / V;
+  T x[kPerLane];
+  template <int LPR, bool TAIL>
+  __device__ __forceinline__ void load(const T* p, int lane, int H) {
+    typedef typename Vec<T>::type TV;
 #pragma unroll
-  for (int c = 0; c < kPerLane / V; ++c) {
-    const int d = (c * LPR + lane) * V;
-    if (d < H) {
-      if constexpr (V == 1) {
-        x[c] = (float)p[d];
-      } else {
-        const TV t = *reinterpret_cast<const TV*>(p + d);
+    for (int c = 0; c < C; ++c) {
+      const int d = (c * LPR + lane) * V;
+      TV t = {};
+      if (TAIL ? d + V <= H : d < H) {
+        t = *reinterpret_cast<const TV*>(p + d);
+      } else if (TAIL && d < H) {
+        if (H >= V) {
+          const Bits b = __builtin_bit_cast(Bits, *reinterpret_cast<const TV*>(p + H - V));
+          t = __builtin_bit_cast(TV, (Bits)(b >> 8 * (int)sizeof(T) * (d + V - H)));
+        } else {
 #pragma unroll
-        for (int k = 0; k < V; ++k) x[c * V + k] = (float)t[k];
+          for (int k = 0; k < V - 1; ++k)
+            if (d + k < H) t[k] = p[d + k];
+        }
       }
-    } else {
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[c * V + k] = 0.f;
+      for (int k = 0; k < V; ++k) x[c * V + k] = t[k];
     }
   }
+};
+template <typename T, int LPR, bool TAIL>
+__device__ __forceinline__ void load_row(const T* p, int lane, int H, float (&x)[kPerLane]) {
+  Raw<T> r;
+  r.template load<LPR, TAIL>(p, lane, H);
+#pragma unroll
+  for (int e = 0; e < kPerLane; ++e) x[e] = (float)r.x[e];
 }
 
-template <typename T, int V, int LPR>
+// Stores the low bits of b as a U and drops them.
+template <typename U, typename T>
+__device__ __forceinline__ T* put(T* p, Bits& b) {
+  typedef U Any __attribute__((aligned(sizeof(T)), may_alias));
+  *reinterpret_cast<Any*>(p) = (U)b;
+  b >>= 8 * sizeof(U);
+  return p + sizeof(U) / sizeof(T);
+}
+
+// V: elements a lane holds side by side, which the loads of the row's type set.
+template <typename T, int V, int LPR, bool TAIL>
 __device__ __forceinline__ void store_row(T* p, int lane, int H, const float (&x)[kPerLane]) {
-  typedef T TV __attribute__((ext_vector_type(V)));
+  typedef T TV __attribute__((ext_vector_type(V), aligned(sizeof(T))));
 #pragma unroll
   for (int c = 0; c < kPerLane / V; ++c) {
     const int d = (c * LPR + lane) * V;
-    if (d < H) {
-      if constexpr (V == 1) {
-        p[d] = (T)x[c];
-      } else {
-        TV t;
+    TV t;
 #pragma unroll
-        for (int k = 0; k < V; ++k) t[k] = (T)x[c * V + k];
-        *reinterpret_cast<TV*>(p + d) = t;
+    for (int k = 0; k < V; ++k) t[k] = (T)x[c * V + k];
+    if (TAIL ? d + V <= H : d < H) {
+      *reinterpret_cast<TV*>(p + d) = t;
+    } else if (TAIL && d < H) {
+      if constexpr (sizeof(TV) == sizeof(Bits)) {
+        Bits b = __builtin_bit_cast(Bits, t);
+        T* q = p + d;
+        const int left = (H - d) * (int)sizeof(T);  // bytes; the same for every row
+        if (left & 8) q = put<uint64_t>(q, b);
+        if (left & 4) q = put<uint32_t>(q, b);
+        if (left & 2) put<uint16_t>(q, b);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V - 1; ++k)
+          if (d + k < H) p[d + k] = t[k];
       }
     }
   }
@@ -122,20 +167,19 @@ __device__ __forceinline__ bool inside(int e, int lane, int H) {
 }
 
 template <int LPR>
-constexpr int threads_of = LPR > NT ? LPR : NT;
+constexpr int threads_of = LPR > NT / 2 ? LPR : NT;
 
-template <typename T, int V, int LPR>
+template <typename T, int LPR, bool TAIL>
 __global__ __launch_bounds__(threads_of<LPR>) void norm_fwd_kernel(NormFwd a) {
-  constexpr int slots = threads_of<LPR> / LPR;
+  constexpr int slots = threads_of<LPR> / LPR, V = vec_of<T>;
   __shared__ float red[threads_of<LPR> / 64];
   const int H = a.H, lane = threadIdx.x % LPR;
   const float inv = 1.f / (float)H;
   const int64_t row = (int64_t)blockIdx.x * slots + threadIdx.x / LPR;
   const bool in = row < a.N;
-  float x[kPerLane], w[kPerLane], b[kPerLane];
-  load_row<T, V, LPR>((const T*)a.x + (in ? row : 0) * H, lane, H, x);
-  load_row<T, V, LPR>((const T*)a.w, lane, H, w);
-  if (a.b) load_row<T, V, LPR>((const T*)a.b, lane, H, b);
+  float x[kPerLane], w[kPerLane];
+  load_row<T, LPR, TAIL>((const T*)a.x + (in ? row : 0) * H, lane, H, x);
+  load_row<T, LPR, TAIL>((const T*)a.w, lane, H, w);
   float mu = 0.f;
   if (!a.rms) {
     float s = 0.f;
@@ -151,8 +195,13 @@ __global__ __launch_bounds__(threads_of<LPR>) void norm_fwd_kernel(NormFwd a) {
   const float rstd = 1.f / sqrtf(row_sum<LPR>(q, red) * inv + a.eps);
   if (!in) return;
 #pragma unroll
-  for (int e = 0; e < kPerLane; ++e) x[e] = x[e] * rstd * w[e] + (a.b ? b[e] : 0.f);
-  store_row<T, V, LPR>((T*)a.y + row * H, lane, H, x);
+  for (int e = 0; e < kPerLane; ++e) x[e] = x[e] * rstd * w[e];
+  if (a.b) {
+    load_row<T, LPR, TAIL>((const T*)a.b, lane, H, w);
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) x[e] += w[e];
+  }
+  store_row<T, V, LPR, TAIL>((T*)a.y + row * H, lane, H, x);
   if (lane == 0) {
     if (a.mean) a.mean[row] = mu;
     if (a.rstd) a.rstd[row] = rstd;
@@ -161,29 +210,33 @@ __global__ __launch_bounds__(threads_of<LPR>) void norm_fwd_kernel(NormFwd a) {
 
 // Each workgroup takes every gridDim.x-th set of rows and adds up its part of
 // dw and db in registers, then over its rows in LDS: one partial row each a
-// workgroup, added up by norm_bwd_reduce_kernel.
-template <typename T, int V, int LPR>
-__global__ __launch_bounds__(threads_of<LPR>) void norm_bwd_kernel(NormBwd a) {
-  constexpr int slots = threads_of<LPR> / LPR;
+// workgroup, added up by norm_bwd_reduce_kernel. What lies past H has x, dy and
+// w of 0 and adds nothing.
+// (bf16 rows are half as many bytes, so it takes four waves a SIMD rather
+// than three to keep enough in flight: 65536 x 896, 79 us against 105.)
+template <typename T, int LPR, bool TAIL>
+__global__ __launch_bounds__(threads_of<LPR>, sizeof(T) == 4 ? 1 : 4) void norm_bwd_kernel(NormBwd a) {
+  constexpr int slots = threads_of<LPR> / LPR, V = vec_of<T>;
   __shared__ float red[threads_of<LPR> / 64];
   __shared__ alignas(32) float sums[slots > 1 ? NT * kPerLane : 1];
   const int H = a.H, lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
   const float inv = 1.f / (float)H;
   float w[kPerLane], gw[kPerLane], gb[kPerLane];
-  load_row<T, V, LPR>((const T*)a.w, lane, H, w);
+  load_row<T, LPR, TAIL>((const T*)a.w, lane, H, w);
 #pragma unroll
   for (int e = 0; e < kPerLane; ++e) gw[e] = gb[e] = 0.f;
-  for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.N; r0 += (int64_t)gridDim.x * slots) {  // uniform
-    const int64_t row = r0 + slot;
-    const bool in = row < a.N;
+  const int64_t stride = (int64_t)gridDim.x * slots;
+  for (int64_t r0 = (int64_t)blockIdx.x * slots; r0 < a.N; r0 += stride) {  // uniform
+    const int64_t row = r0 + slot, at = row < a.N ? row : 0;
+    const int h = row < a.N ? H : 0;
     float x[kPerLane], gy[kPerLane];
-    load_row<T, V, LPR>((const T*)a.x + (in ? row : 0) * H, lane, in ? H : 0, x);
-    load_row<T, V, LPR>((const T*)a.gy + (in ? row : 0) * H, lane, in ? H : 0, gy);
-    const float rstd = in ? a.rstd[row] : 0.f, mu = a.rms || !in ? 0.f : a.mean[row];
+    load_row<T, LPR, TAIL>((const T*)a.x + at * H, lane, h, x);
+    load_row<T, LPR, TAIL>((const T*)a.gy + at * H, lane, h, gy);
+    const float rstd = h ? a.rstd[at] : 0.f, mu = a.rms || !h ? 0.f : a.mean[at];
     float s = 0.f, q = 0.f;
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
-      x[e] = inside<V, LPR>(e, lane, H) ? (x[e] - mu) * rstd : 0.f;
+      x[e] = (x[e] - mu) * rstd;
       const float c = gy[e] * w[e];
       s += c;
       q += c * x[e];
@@ -195,17 +248,17 @@ __global__ __launch_bounds__(threads_of<LPR>) void norm_bwd_kernel(NormBwd a) {
     const float mq = row_sum<LPR>(q, red) * inv;
 #pragma unroll
     for (int e = 0; e < kPerLane; ++e) x[e] = rstd * (gy[e] * w[e] - mc - x[e] * mq);
-    if (in) store_row<T, V, LPR>((T*)a.gx + row * H, lane, H, x);
+    if (row < a.N) store_row<T, V, LPR, TAIL>((T*)a.gx + row * H, lane, H, x);
   }
   if (!a.part) return;
   float* out = a.part + (int64_t)blockIdx.x * H;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {  // dw, then db
     if (slots == 1) {
-      store_row<float, V, LPR>(out, lane, H, k ? gb : gw);
+      store_row<float, V, LPR, TAIL>(out, lane, H, k ? gb : gw);
     } else {
       __syncthreads();
-      store_row<float, V, LPR>(sums + slot * H, lane, H, k ? gb : gw);
+      store_row<float, V, LPR, TAIL>(sums + slot * H, lane, H, k ? gb : gw);
       __syncthreads();
       for (int d = threadIdx.x; d < H; d += NT) {
         float t = 0.f;
@@ -318,14 +371,10 @@ __global__ __launch_bounds__(kReduceCols* kReduceRows) void norm_bwd_reduce_kern
 
 // Lanes that share a row of H.
 int lanes_of(int H) {
-  int l = 8;
-  while (l * kPerLane < H) l *= 2;
-  return l;
-}
-
-template <typename... P>
-bool aligned16(P... p) {
-  return (((uintptr_t)p | ...) & 15) == 0;
+  const int need = (H + kPerLane - 1) / kPerLane;
+  for (int l : {8, 16, 32, 64, 128, 192, 256, 320, 384, 512, 640, 768})
+    if (l >= need) return l;
+  return kMaxLanes;
 }
 
 // f(std::integral_constant<int, LPR>) for the row's lanes.
@@ -337,43 +386,53 @@ hipError_t with_lanes(int H, F f) {
     case 32: return f(std::integral_constant<int, 32>());
     case 64: return f(std::integral_constant<int, 64>());
     case 128: return f(std::integral_constant<int, 128>());
+    case 192: return f(std::integral_constant<int, 192>());
     case 256: return f(std::integral_constant<int, 256>());
+    case 320: return f(std::integral_constant<int, 320>());
+    case 384: return f(std::integral_constant<int, 384>());
     case 512: return f(std::integral_constant<int, 512>());
-    default: return f(std::integral_constant<int, 1024>());
+    case 640: return f(std::integral_constant<int, 640>());
+    case 768: return f(std::integral_constant<int, 768>());
+    default: return f(std::integral_constant<int, kMaxLanes>());
   }
 }
 
-template <typename T, int V>
+template <typename T>
 hipError_t norm_fwd_rows(const NormFwd& a, hipStream_t st) {
   return with_lanes(a.H, [&](auto lanes) {
     constexpr int LPR = decltype(lanes)::value, slots = threads_of<LPR> / LPR;
-    norm_fwd_kernel<T, V, LPR><<<(unsigned)((a.N + slots - 1) / slots), threads_of<LPR>, 0, st>>>(a);
+    const unsigned grid = (unsigned)((a.N + slots - 1) / slots);
+    if (a.H % vec_of<T>)
+      norm_fwd_kernel<T, LPR, true><<<grid, threads_of<LPR>, 0, st>>>(a);
+    else
+      norm_fwd_kernel<T, LPR, false><<<grid, threads_of<LPR>, 0, st>>>(a);
     return hipGetLastError();
   });
 }
 
-template <typename T, int V>
+template <typename T>
 hipError_t norm_bwd_rows(const NormBwd& a, int groups, hipStream_t st) {
   return with_lanes(a.H, [&](auto lanes) {
     constexpr int LPR = decltype(lanes)::value;
-    norm_bwd_kernel<T, V, LPR><<<groups, threads_of<LPR>, 0, st>>>(a);
+    if (a.H % vec_of<T>)
+      norm_bwd_kernel<T, LPR, true><<<groups, threads_of<LPR>, 0, st>>>(a);
+    else
+      norm_bwd_kernel<T, LPR, false><<<groups, threads_of<LPR>, 0, st>>>(a);
     return hipGetLastError();
   });
 }
 
 template <typename T>
 hipError_t norm_fwd(const NormFwd& a, hipStream_t st) {
-  constexpr int V = 16 / sizeof(T);
   if (a.H > kMaxLanes * kPerLane) {
     norm_fwd_any_kernel<T><<<(unsigned)std::min<int64_t>(a.N, 65536), NT, 0, st>>>(a);
     return hipGetLastError();
   }
-  return a.H % V == 0 && aligned16(a.x, a.w, a.b, a.y) ? norm_fwd_rows<T, V>(a, st) : norm_fwd_rows<T, 1>(a, st);
+  return norm_fwd_rows<T>(a, st);
 }
 
 template <typename T>
 hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
-  constexpr int V = 16 / sizeof(T);
   const int groups = norm_bwd_groups(a.N, a.H);
   if (a.H > kMaxLanes * kPerLane) {
     if (a.gx && a.N > 0) {
@@ -385,9 +444,7 @@ hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
       if (hipError_t e = hipGetLastError()) return e;
     }
   } else if (a.N > 0 || a.part) {
-    const hipError_t e = a.H % V == 0 && aligned16(a.x, a.w, a.gy, a.gx, a.part) ? norm_bwd_rows<T, V>(a, groups, st)
-                                                                                 : norm_bwd_rows<T, 1>(a, groups, st);
-    if (e != hipSuccess) return e;
+    if (hipError_t e = norm_bwd_rows<T>(a, groups, st)) return e;
   }
   if (a.part)
     norm_bwd_reduce_kernel<T><<<dim3((a.H + kReduceCols - 1) / kReduceCols, 2), kReduceCols * kReduceRows, 0, st>>>(
@@ -397,9 +454,14 @@ hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
 
 }  // namespace
 
+// More groups hide more latency, fewer leave less to add up at the end: 768
+// where several rows share a workgroup, else 512 (65536 x 896 bf16: 78 us with
+// 512, 72 with 768, 75 with 1024; 16384 x 4096 fp32: 157, 162 and 165 us).
+// The partial sums stay below 32 MB however long the row.
 int norm_bwd_groups(int64_t N, int H) {
   const int lanes = lanes_of(H), slots = lanes < NT ? NT / lanes : 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(512, (N + slots - 1) / slots));
+  const int most = std::min(slots > 1 ? 768 : 512, std::max(64, (4 << 20) / H));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, (N + slots - 1) / slots));
 }
 
 hipError_t launch_norm_fwd(const NormFwd& a, hipStream_t st) {

@@ -203,8 +203,6 @@ PLP_API int plp_adamw_step(const plp_adamw_args* a, const plp_adamw_tensor* tens
     d.param_bf16 = t.param_dtype == PLP_DTYPE_BF16;
     d.grad_bf16 = t.grad_dtype == PLP_DTYPE_BF16;
     d.bits8 = t.state_bits == 8;
-    d.wide = !(misaligned(t.param, 16) || misaligned(t.grad, 16) || misaligned(t.master, 16) ||
-               misaligned(t.exp_avg, 16) || misaligned(t.exp_avg_sq, 16));
     l.first[l.count + 1] = l.first[l.count] + groups;
     ++l.count;
   }

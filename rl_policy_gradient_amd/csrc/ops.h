@@ -45,7 +45,7 @@ struct AdamTensor {
   float *ms, *vs;      // 8-bit states: one scale per kAdamBlock elements
   int64_t n;
   float decay;         // 1 - lr weight_decay (weight_decay when the rate is read on the device)
-  uint8_t param_bf16, grad_bf16, bits8, wide;  // wide: every array 16-byte aligned
+  uint8_t param_bf16, grad_bf16, bits8;
 };
 constexpr int kAdamBlock = 256;   // elements of one scale
 constexpr int kAdamTile = 1024;   // elements a workgroup takes
