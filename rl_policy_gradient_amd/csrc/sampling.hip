@@ -919,6 +919,7 @@ struct RowSampler {
         pass(nact, zl, zh);
         if (!limits) return place;
         lo = last_place(max(lowest, Key<T>::of(zl)));  // at or below every place listed
+        if (zh < INFINITY) hi = last_place(Key<T>::of(zh)) | kIndexMask;  // at or above
         whole = whole && zl == L;
       } else {
         whole = false;
