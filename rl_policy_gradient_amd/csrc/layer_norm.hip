@@ -401,12 +401,23 @@ template <typename T>
 hipError_t norm_fwd_rows(const NormFwd& a, hipStream_t st) {
   return with_lanes(a.H, [&](auto lanes) {
     constexpr int LPR = decltype(lanes)::value, slots = threads_of<LPR> / LPR;
-    const unsigned grid = (unsigned)((a.N + slots - 1) / slots);
-    if (a.H % vec_of<T>)
-      norm_fwd_kernel<T, LPR, true><<<grid, threads_of<LPR>, 0, st>>>(a);
-    else
-      norm_fwd_kernel<T, LPR, false><<<grid, threads_of<LPR>, 0, st>>>(a);
-    return hipGetLastError();
+    // a launch holds fewer than 2^32 threads
+    constexpr int64_t most = ((int64_t)1 << 31) / threads_of<LPR> * slots;
+    NormFwd b = a;
+    for (int64_t left = a.N; left > 0; left -= most) {
+      b.N = std::min(left, most);
+      const unsigned grid = (unsigned)((b.N + slots - 1) / slots);
+      if (a.H % vec_of<T>)
+        norm_fwd_kernel<T, LPR, true><<<grid, threads_of<LPR>, 0, st>>>(b);
+      else
+        norm_fwd_kernel<T, LPR, false><<<grid, threads_of<LPR>, 0, st>>>(b);
+      if (hipError_t e = hipGetLastError()) return e;
+      b.x = (const T*)b.x + b.N * a.H;
+      b.y = (T*)b.y + b.N * a.H;
+      if (b.mean) b.mean += b.N;
+      if (b.rstd) b.rstd += b.N;
+    }
+    return hipSuccess;
   });
 }
 

@@ -272,3 +272,49 @@ def test_other_stream():
     s.synchronize()
     assert torch.equal(got, want)
     assert np.isfinite(want.float().sum().item())
+
+
+def test_more_rows_than_one_launch_holds():
+    """2^29 + 5 rows: 8 lanes a row, so more threads than a launch can have."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    N = 2 ** 29 + 5
+    x = torch.empty(N, 1, dtype=torch.bfloat16, device="cuda")
+    x.view(torch.int16).copy_((torch.arange(N, device="cuda", dtype=torch.int32) % 0x0701 + 0x3c00).to(torch.int16)[:, None])
+    w = torch.full((1,), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = plp.layer_norm_fwd(x, w, eps=1.0, rms=True)
+    for i in range(0, N, 2 ** 27):
+        v = x[i:i + 2 ** 27, 0].double()
+        r = (v * v + 1.0).rsqrt()
+        # rstd: the square, the sum, the root and the quotient, half a step each; y: two products and the rounding
+        assert ((out["rstd"][i:i + 2 ** 27].double() - r).abs() <= 4 * 2.0 ** -24 * r).all(), i
+        y = 3.0 * v * r
+        assert ((out["y"][i:i + 2 ** 27, 0].double() - y).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * y.abs()).all(), i
+
+
+def test_offsets_past_32_bits():
+    """2.7e9 elements, forward and backward; whole-number gradients, so that
+    grad_bias is exact."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    N, H = 3_000_001, 896
+    g = torch.Generator().manual_seed(3)
+    few = torch.randn(1009, H, generator=g).to(torch.bfloat16).cuda()
+    gyf = torch.randint(-1, 2, (1009, H), generator=g).to(torch.bfloat16).cuda()
+    w = torch.randn(H, generator=g).to(torch.bfloat16).cuda()
+    reps = -(-N // 1009)
+    x, gy = few.repeat(reps, 1)[:N], gyf.repeat(reps, 1)[:N]
+    out = plp.layer_norm_fwd(x, w)
+    gr = plp.layer_norm_bwd(gy, x, w, out["rstd"], out["mean"])
+    # the same rows in a small batch give the same bits
+    small = plp.layer_norm_fwd(few, w)
+    sgx = plp.layer_norm_bwd(gyf, few, w, small["rstd"], small["mean"])["grad_x"]
+    for i in range(0, N, 1009 * 500):
+        n = min(1009 * 500, N - i)
+        at = torch.arange(n, device="cuda") % 1009
+        for got, want in ((out["y"], small["y"]), (out["mean"], small["mean"]), (out["rstd"], small["rstd"]),
+                          (gr["grad_x"], sgx)):
+            assert torch.equal(got[i:i + n], want[at]), i
+    last = N - (reps - 1) * 1009
+    gb = gyf.double().sum(0) * (reps - 1) + gyf[:last].double().sum(0)
+    assert torch.equal(gr["grad_bias"], gb.to(torch.bfloat16))
