@@ -317,15 +317,17 @@ PLP_API int plp_policy_loss_from_logprobs(const plp_args* args, const float* log
 /* ---- Operators around the fused loss ---------------------------------------
  * The other calls of a policy's training loop: sampling the completions (the
  * targets and their old_logp), the final norm that gives `hidden` and takes
- * grad_hidden back, and the AdamW step that takes grad_weight and grad_bias. They follow the conventions above, but for alignment: a tensor needs only the alignment of
- * its elements (16-byte aligned rows take the wide path). These entry points
- * were added to ABI version 5, whose existing calls are unchanged. */
+ * grad_hidden back, and the AdamW step that takes grad_weight and grad_bias.
+ * They follow the conventions above, but for alignment: a tensor needs only
+ * the alignment of its elements. Outputs that share memory with an input or
+ * with each other are refused (PLP_E_INVALID). These entry points were added
+ * to ABI version 5, whose existing calls are unchanged. */
 
 /* Layer norm over rows of H: mu = mean(x), rstd = 1/sqrt(mean((x-mu)^2) + eps),
  * y = (x - mu) rstd w + b; with rms nonzero mu = 0 (root-mean-square norm).
  * x, y [N,H], weight, bias [H] of `dtype`; bias may be NULL. Statistics in
  * fp32: mean_out [N] (NULL with rms), rstd_out [N], each NULL to skip; the
- * backward reads them. N = 0 does nothing. y must not overlap an input.
+ * backward reads them. N = 0 does nothing.
  * Errors: PLP_E_INVALID (sizes, NULLs, eps negative or not finite, overlap,
  * mean_out with rms), PLP_E_UNSUPPORTED (H > 65536), PLP_E_HIP. */
 PLP_API int plp_layer_norm_fwd(const void* x, const void* weight, const void* bias, int64_t N, int32_t H,
@@ -337,8 +339,7 @@ PLP_API int plp_layer_norm_fwd(const void* x, const void* weight, const void* bi
  * without mean(c) for rms; grad_weight = sum over rows of grad_y xh,
  * grad_bias = sum over rows of grad_y, both summed in fp32 in a fixed order.
  * Each gradient may be NULL to skip it; the workspace is needed for
- * grad_weight or grad_bias only. N = 0 gives zero grad_weight and grad_bias.
- * No gradient may overlap an input or another gradient. */
+ * grad_weight or grad_bias only. N = 0 gives zero grad_weight and grad_bias. */
 PLP_API int plp_layer_norm_bwd_workspace_size(int64_t N, int32_t H, int32_t dtype, size_t* bytes);
 PLP_API int plp_layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const float* mean,
                                const float* rstd, int64_t N, int32_t H, int32_t dtype, int32_t rms, void* grad_x,

@@ -24,6 +24,24 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// No output may share a byte with an input or with another output.
+template <size_t I, size_t O>
+int check_apart(const Range (&in)[I], const Range (&out)[O]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (const Range& q : in)
+      if (overlap(out[i].p, out[i].n, q.p, q.n)) return fail(PLP_E_INVALID, "an output must not overlap an input");
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(PLP_E_INVALID, "outputs must not overlap each other");
+  }
+  return PLP_OK;
+}
+
 // Workgroups of one AdamW launch (times 256 threads stays below 2^32), and the
 // largest tensor, which fits one.
 constexpr int64_t kMaxAdamGrid = (int64_t)1 << 23;
@@ -53,10 +71,7 @@ int check_adamw_tensor(const plp_adamw_tensor& t, int i) {
   if (misaligned(t.param, pe) || misaligned(t.grad, ge) || misaligned(t.master, 4) || misaligned(t.exp_avg, se) ||
       misaligned(t.exp_avg_sq, se) || misaligned(t.exp_avg_scale, 4) || misaligned(t.exp_avg_sq_scale, 4))
     return fail(PLP_E_INVALID, "tensor %d: an array is not aligned to its elements", i);
-  const struct {
-    const void* p;
-    size_t n;
-  } r[] = {{t.param, n * pe},        {t.master, n * 4},           {t.exp_avg, n * se}, {t.exp_avg_sq, n * se},
+  const Range r[] = {{t.param, n * pe},        {t.master, n * 4},           {t.exp_avg, n * se}, {t.exp_avg_sq, n * se},
            {t.exp_avg_scale, sb}, {t.exp_avg_sq_scale, sb}, {t.grad, n * ge}};
   for (int x = 0; x < 7; ++x)
     for (int y = 0; y < x; ++y)
@@ -95,11 +110,13 @@ PLP_API int plp_layer_norm_fwd(const void* x, const void* weight, const void* bi
   if (rms && mean_out) return fail(PLP_E_INVALID, "the norm without a mean (rms) has no mean_out");
   if (N == 0) return ok();
   if (!x || !y) return fail(PLP_E_INVALID, "x and y are required");
-  const size_t e = esize(dtype), xb = (size_t)N * H * e;
-  if (misaligned(x, e) || misaligned(y, e) || misaligned(weight, e) || misaligned(bias, e))
+  const size_t e = esize(dtype), xb = (size_t)N * H * e, sb = (size_t)N * sizeof(float);
+  if (misaligned(x, e) || misaligned(y, e) || misaligned(weight, e) || misaligned(bias, e) || misaligned(mean_out, 4) ||
+      misaligned(rstd_out, 4))
     return fail(PLP_E_INVALID, "a tensor is not aligned to its elements");
-  if (overlap(y, xb, x, xb) || overlap(y, xb, weight, H * e) || overlap(y, xb, bias, H * e))
-    return fail(PLP_E_INVALID, "y must not overlap an input");
+  const Range in[] = {{x, xb}, {weight, H * e}, {bias, H * e}}, out[] = {{y, xb}, {mean_out, sb}, {rstd_out, sb}};
+  rc = check_apart(in, out);
+  if (rc) return rc;
   HIP_TRY(launch_norm_fwd(NormFwd{x, weight, bias, y, mean_out, rstd_out, N, H, dtype, rms ? 1 : 0, (float)eps}, st));
   return ok();
 }
@@ -125,19 +142,13 @@ PLP_API int plp_layer_norm_bwd(const void* grad_y, const void* x, const void* we
     return fail(PLP_E_INVALID, "grad_y, x, rstd and (but for rms) mean are required");
   const size_t e = esize(dtype), xb = (size_t)N * H * e, wb = (size_t)H * e;
   if (misaligned(grad_y, e) || misaligned(x, e) || misaligned(weight, e) || misaligned(grad_x, e) ||
-      misaligned(grad_weight, e) || misaligned(grad_bias, e))
+      misaligned(grad_weight, e) || misaligned(grad_bias, e) || misaligned(mean, 4) || misaligned(rstd, 4))
     return fail(PLP_E_INVALID, "a tensor is not aligned to its elements");
-  const struct {
-    const void* p;
-    size_t n;
-  } in[] = {{grad_y, xb}, {x, xb}, {weight, wb}}, out[] = {{grad_x, xb}, {grad_weight, wb}, {grad_bias, wb}};
-  for (int i = 0; i < 3; ++i) {
-    for (const auto& q : in)
-      if (overlap(out[i].p, out[i].n, q.p, q.n)) return fail(PLP_E_INVALID, "a gradient must not overlap an input");
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
-        return fail(PLP_E_INVALID, "the gradients must not overlap each other");
-  }
+  const size_t sb = (size_t)N * sizeof(float);
+  const Range in[] = {{grad_y, xb}, {x, xb}, {weight, wb}, {rms ? nullptr : mean, sb}, {rstd, sb}},
+              out[] = {{grad_x, xb}, {grad_weight, wb}, {grad_bias, wb}};
+  rc = check_apart(in, out);
+  if (rc) return rc;
   rc = check_ws(ws, ws_bytes, grad_weight || grad_bias ? need : 0);
   if (rc) return rc;
   HIP_TRY(launch_norm_bwd(NormBwd{grad_y, x, weight, mean, rstd, grad_x, grad_weight, grad_bias,
@@ -245,6 +256,16 @@ PLP_API int plp_sample_tokens(const plp_sample_args* a, void* ws, size_t ws_byte
     if (misaligned(p, 4)) return fail(PLP_E_INVALID, "an array is not aligned to its elements");
   if (misaligned(a->logits, esize(a->dtype)) || misaligned(a->token_out, 8))
     return fail(PLP_E_INVALID, "an array is not aligned to its elements");
+  int64_t span = 0;  // bytes from the first row's start to the last one's end
+  if (__builtin_mul_overflow(a->N - 1, a->row_stride, &span) || __builtin_add_overflow(span, (int64_t)a->V, &span) ||
+      __builtin_mul_overflow(span, (int64_t)esize(a->dtype), &span))
+    return fail(PLP_E_INVALID, "row_stride=%lld is past the address space", (long long)a->row_stride);
+  const size_t rb = (size_t)a->N * 4;
+  const Range in[] = {{a->logits, (size_t)span},  {a->uniforms, rb},   {a->temperature_rows, rb},
+                      {a->top_k_rows, rb},        {a->top_p_rows, rb}, {a->min_p_rows, rb}},
+              out[] = {{a->token_out, rb * 2}, {a->logp_out, rb}, {a->kept_logp_out, rb}};
+  rc = check_apart(in, out);
+  if (rc) return rc;
   rc = check_ws(ws, ws_bytes, need);
   if (rc) return rc;
   SampleArgs s;

@@ -3,9 +3,9 @@
 ``sample_tokens`` draws the completions, with the log-probs the loss takes as
 old_logp; ``layer_norm_fwd`` gives the hidden states the fused loss takes and
 ``layer_norm_bwd`` takes its grad_hidden back; ``adamw_step`` takes the
-gradients of the weights, over every tensor of the model at once. Like the rest of the package
-these are bindings: the work is done by HIP kernels behind include/plp.h,
-enqueued on the current stream of the tensors' device.
+gradients of the weights, over every tensor of the model at once. Like the
+rest of the package these are bindings: the work is done by HIP kernels behind
+include/plp.h, enqueued on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
@@ -29,6 +29,15 @@ def _out(out: Optional[dict], name: str, shape, dtype, dev) -> torch.Tensor:
     return t
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _fits(n: int, name: str) -> None:
+    """The C ABI holds row lengths in 32 bits."""
+    if n > _INT32_MAX:
+        raise ValueError(f"{name}={n} is above {_INT32_MAX}")
+
+
 def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: Union[float, torch.Tensor] = 1.0,
                   top_k: Union[int, torch.Tensor] = 0, top_p: Union[float, torch.Tensor] = 1.0,
                   min_p: Union[float, torch.Tensor] = 0.0, workspace: Optional[torch.Tensor] = None,
@@ -49,6 +58,7 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
     dev = _one_device((("logits", logits), ("uniforms", uniforms), ("workspace", workspace), *rows.items()))
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("plp needs each row of logits contiguous")
+    _fits(V, "V")
     _check_vec(uniforms, N, torch.float32, "uniforms")
     for k, t in rows.items():
         _check_vec(t, N, torch.int32 if k == "top_k" else torch.float32, k)
@@ -63,7 +73,7 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
     if "top_k" in rows:
         a.top_k_rows = _ptr(top_k)
     else:
-        a.top_k = int(top_k)
+        a.top_k = max(-1, min(int(top_k), _INT32_MAX))
     if "top_p" in rows:
         a.top_p_rows = _ptr(top_p)
     else:
@@ -80,13 +90,14 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
                "kept_logp": _out(out, "kept_logp", (N,), torch.float32, dev)}
         a.token_out, a.logp_out, a.kept_logp_out = _ptr(res["token"]), _ptr(res["logp"]), _ptr(res["kept_logp"])
         ws = _workspace(n.value, dev, workspace)
-        _abi.check(L.plp_sample_tokens(ctypes.byref(a), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(dev)))
+        _abi.check(L.plp_sample_tokens(ctypes.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev)))
     return res
 
 
 def _norm_sizes(x, weight, bias):
     *rows, H = x.shape
     N = math.prod(rows)
+    _fits(H, "H")
     for name, t in (("weight", weight), ("bias", bias)):
         if t is not None and (t.shape != (H,) or t.dtype != x.dtype):
             raise ValueError(f"{name}: expected ({H},) {x.dtype}, got {tuple(t.shape)} {t.dtype}")
@@ -144,7 +155,7 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
         ws = _workspace(n.value if grad_weight or grad_bias else 0, dev, workspace)
         _abi.check(L.plp_layer_norm_bwd(_ptr(grad_y), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), N, H, dt,
                                         1 if rms else 0, _ptr(res.get("grad_x")), _ptr(res.get("grad_weight")),
-                                        _ptr(res.get("grad_bias")), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                        _ptr(res.get("grad_bias")), _ptr(ws), ws.numel() * ws.element_size(),
                                         _stream_on(dev)))
     return res
 

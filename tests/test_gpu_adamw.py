@@ -331,3 +331,29 @@ def test_table_refuses():
         with pytest.raises(plp.PlpError):
             plp.adamw_step(table, **kw)
     plp.adamw_step(plp.adamw_table([], [], []), lr=1e-3, step=1)
+
+
+def test_more_than_2_to_the_32_elements():
+    """One tensor of 2^32 + 777 elements: its blocks repeat every 2^20, and so
+    do the results."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    n, period = 2 ** 32 + 777, 2 ** 20
+    g = torch.Generator().manual_seed(5)
+    p1, g1 = (torch.randn(period, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    reps = -(-n // period)
+    p, gr = p1.repeat(reps)[:n], g1.repeat(reps)[:n]
+    st, st1 = plp.adamw_state(p, bits=8), plp.adamw_state(p1, bits=8)
+    for a, b, s in ((p, gr, st), (p1, g1, st1)):
+        table = plp.adamw_table([a], [b], [s], weight_decay=0.01)
+        for step in (1, 2):
+            plp.adamw_step(table, lr=1e-2, step=step)
+    whole = (n // period) * period
+    assert (p[:whole].view(-1, period) == p1).all()
+    assert torch.equal(p[whole:whole + 768], p1[:768])  # whole blocks of the last 777
+    for k in ("exp_avg", "exp_rms"):
+        a, b = st[k].view(torch.uint8), st1[k].view(torch.uint8)
+        assert (a[:whole].view(-1, period) == b).all(), k
+        assert torch.equal(a[whole:whole + 768], b[:768]), k
+        s, s1 = st[k + "_scale"], st1[k + "_scale"]
+        assert (s[:whole // 256].view(-1, period // 256) == s1).all() and torch.equal(s[whole // 256:][:3], s1[:3]), k

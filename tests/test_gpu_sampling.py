@@ -313,3 +313,64 @@ def test_captured_and_replayed():
         want = plp.sample_tokens(z, u, temperature=tau, top_k=k, top_p=0.9)
         for n in want:
             assert torch.equal(out[n], want[n]), (i, n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_huge_magnitudes(dtype):
+    """Logits up to the type's largest and lowest, whose differences overflow fp32."""
+    require_gpu()
+    g = torch.Generator().manual_seed(31)
+    for V in (700, 9000, 40000):
+        z = (torch.rand(6, V, generator=g, dtype=torch.float64) * 2 - 1) * 3.38e38
+        z[1, ::2] = torch.finfo(DT[dtype]).max
+        z[2] = torch.finfo(DT[dtype]).min
+        z[3, : V // 2] = torch.finfo(DT[dtype]).min
+        z[4, 5:] = -1e30
+        z = z.to(DT[dtype])
+        u = torch.rand(6, generator=g)
+        for tau in (1.0, 1e37, 3e38):
+            for k, p, mp in ((0, 1.0, 0.0), (50, 1.0, 0.0), (0, 0.9, 0.0), (3000, 0.5, 0.0), (0, 1.0, 0.3), (20, 0.9, 0.1)):
+                check(z, u, tau, k, p, mp)
+
+
+def test_many_rows_and_a_top_k_past_32_bits():
+    """More rows than one launch takes (32768), settings of each row, and a k
+    that a 32-bit argument does not hold (no limit)."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    z, u = logits(70001, 37, "f32", 4)
+    g = torch.Generator().manual_seed(4)
+    k = torch.randint(0, 40, (70001,), generator=g, dtype=torch.int32)
+    check(z, u, 0.9, k, 0.9, 0.0)
+    a, b = plp.sample_tokens(z.cuda(), u.cuda(), top_k=2 ** 32 + 5), plp.sample_tokens(z.cuda(), u.cuda())
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_calls_side_by_side():
+    """Two streams at once, each with its own workspace and outputs."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    zs = [tuple(t.cuda() for t in logits(64, 30000, "bf16", s)) for s in (1, 2)]
+    kws = [dict(top_p=0.9), dict(top_k=50, temperature=0.7)]
+    want = [plp.sample_tokens(*z, **kw) for z, kw in zip(zs, kws)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in zs]
+    got = [[] for _ in zs]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(plp.sample_tokens(*zs[i], **kws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in got[i]:
+            for n in o:
+                assert torch.equal(o[n], want[i][n]), (i, n)
+
+
+def test_workspace_has_to_be_contiguous():
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    z, u = (t.cuda() for t in logits(4, 100, "bf16", 1))
+    with pytest.raises(ValueError, match="contiguous"):
+        plp.sample_tokens(z, u, workspace=torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20))

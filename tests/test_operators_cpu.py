@@ -46,6 +46,10 @@ def norm_fwd(**kw):
     (dict(y=X), abi.PLP_E_INVALID, "overlap"),
     (dict(y=X + 8 * 64 * 2 - 2), abi.PLP_E_INVALID, "overlap"),
     (dict(y=W - 2), abi.PLP_E_INVALID, "overlap"),
+    (dict(mean=Y), abi.PLP_E_INVALID, "overlap each other"),
+    (dict(rstd=X + 8), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(rstd=M + 28), abi.PLP_E_INVALID, "overlap each other"),
+    (dict(mean=M + 2), abi.PLP_E_INVALID, "aligned"),
 ])
 def test_norm_forward_refuses(kw, code, msg):
     assert norm_fwd(**kw) == code
@@ -71,6 +75,9 @@ def norm_bwd(**kw):
     (dict(gx=Y), abi.PLP_E_INVALID, "overlap an input"),
     (dict(gw=W), abi.PLP_E_INVALID, "overlap an input"),
     (dict(gb=B), abi.PLP_E_INVALID, "overlap each other"),
+    (dict(gx=M), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(gw=R + 16), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(rstd=R + 1), abi.PLP_E_INVALID, "aligned"),
     (dict(n=16), abi.PLP_E_WORKSPACE, "too small"),
     (dict(ws=None), abi.PLP_E_WORKSPACE, "NULL"),
     (dict(ws=WS + 128), abi.PLP_E_WORKSPACE, "aligned"),
@@ -198,6 +205,14 @@ def sample(ws=WS, ws_bytes=1 << 24, **kw):
     (dict(logits=X + 1), abi.PLP_E_INVALID, "aligned"),
     (dict(token_out=Y + 4), abi.PLP_E_INVALID, "aligned"),
     (dict(logp_out=M + 2), abi.PLP_E_INVALID, "aligned"),
+    (dict(token_out=X), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(logp_out=X + 7996), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(row_stride=0, logp_out=X + 1996), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(logp_out=W), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(kept_logp_out=G, temperature_rows=G + 12), abi.PLP_E_INVALID, "overlap an input"),
+    (dict(logp_out=M, kept_logp_out=M + 8), abi.PLP_E_INVALID, "overlap each other"),
+    (dict(row_stride=1 << 62), abi.PLP_E_INVALID, "address space"),
+    (dict(row_stride=(1 << 63) - 1), abi.PLP_E_INVALID, "address space"),
     (dict(ws_bytes=64), abi.PLP_E_WORKSPACE, "too small"),
     (dict(ws=None), abi.PLP_E_WORKSPACE, "NULL"),
     (dict(ws=WS + 8), abi.PLP_E_WORKSPACE, "aligned"),
@@ -215,3 +230,14 @@ def test_sampling_of_nothing_and_workspace():
         # a maximum and a sum for each 256 logits, never a copy of them
         assert N * ((V + 255) // 256) * 12 <= n.value <= N * ((V + 262) // 256) * 12 + 512
     assert L.plp_sample_tokens_workspace_size(1, 1, None) == abi.PLP_E_INVALID
+
+
+def test_row_lengths_past_32_bits_are_refused():
+    """The C ABI's row lengths have 32 bits: a longer one must not wrap."""
+    from rl_policy_gradient_amd import operators
+    with pytest.raises(ValueError, match="H=4294967304"):
+        x = torch.empty(1, dtype=torch.bfloat16).expand(1, 2 ** 32 + 8)
+        operators._norm_sizes(x, x[0], None)
+    with pytest.raises(ValueError, match="V="):
+        operators._fits(2 ** 31, "V")
+    operators._fits(2 ** 31 - 1, "V")
