@@ -10,7 +10,6 @@ include/plp.h, enqueued on the current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
-import math
 from typing import Optional, Sequence, Union
 
 import torch
@@ -19,10 +18,11 @@ from . import _abi
 from ._marshal import _check_vec, _dtype_code, _on, _one_device, _ptr, _stream_on, _workspace
 
 
-def _out(out: Optional[dict], name: str, shape, dtype, dev) -> torch.Tensor:
-    """out[name], checked, or a new tensor."""
+def _out(out: Optional[dict], name: str, shape, dtype, dev, like: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[name], checked, or a new tensor. like: a contiguous tensor of that
+    shape and type, if there is one (half the time of describing it)."""
     if out is None or (t := out.get(name)) is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
         raise ValueError(f"out[{name!r}]: expected {tuple(shape)} {dtype} on {dev}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
@@ -86,8 +86,10 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
     n = ctypes.c_size_t()
     _abi.check(L.plp_sample_tokens_workspace_size(N, V, ctypes.byref(n)))
     with _on(dev):
-        res = {"token": _out(out, "token", (N,), torch.int64, dev), "logp": _out(out, "logp", (N,), torch.float32, dev),
-               "kept_logp": _out(out, "kept_logp", (N,), torch.float32, dev)}
+        like = uniforms if uniforms.dim() == 1 else None
+        res = {"token": _out(out, "token", (N,), torch.int64, dev),
+               "logp": _out(out, "logp", (N,), torch.float32, dev, like),
+               "kept_logp": _out(out, "kept_logp", (N,), torch.float32, dev, like)}
         a.token_out, a.logp_out, a.kept_logp_out = _ptr(res["token"]), _ptr(res["logp"]), _ptr(res["kept_logp"])
         ws = _workspace(n.value, dev, workspace)
         _abi.check(L.plp_sample_tokens(ctypes.byref(a), _ptr(ws), ws.numel() * ws.element_size(), _stream_on(dev)))
@@ -95,8 +97,8 @@ def sample_tokens(logits: torch.Tensor, uniforms: torch.Tensor, *, temperature: 
 
 
 def _norm_sizes(x, weight, bias):
-    *rows, H = x.shape
-    N = math.prod(rows)
+    H = x.shape[-1]
+    N = x.numel() // H if H else 0
     _fits(H, "H")
     for name, t in (("weight", weight), ("bias", bias)):
         if t is not None and (t.shape != (H,) or t.dtype != x.dtype):
@@ -115,9 +117,10 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     dev = _one_device((("x", x), ("weight", weight), ("bias", bias)))
     N, H = _norm_sizes(x, weight, bias)
     with _on(dev):
-        res = {"y": _out(out, "y", x.shape, x.dtype, dev), "rstd": _out(out, "rstd", x.shape[:-1], torch.float32, dev)}
+        res = {"y": _out(out, "y", x.shape, x.dtype, dev, x)}
+        rstd = res["rstd"] = _out(out, "rstd", x.shape[:-1], torch.float32, dev)
         if not rms:
-            res["mean"] = _out(out, "mean", x.shape[:-1], torch.float32, dev)
+            res["mean"] = _out(out, "mean", x.shape[:-1], torch.float32, dev, rstd)
         _abi.check(_abi.lib().plp_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), N, H, _dtype_code(x),
                                                  1 if rms else 0, float(eps), _ptr(res["y"]), _ptr(res.get("mean")),
                                                  _ptr(res["rstd"]), _stream_on(dev)))
@@ -148,10 +151,10 @@ def layer_norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, 
     with _on(dev):
         res = {}
         if grad_x:
-            res["grad_x"] = _out(out, "grad_x", x.shape, x.dtype, dev)
+            res["grad_x"] = _out(out, "grad_x", x.shape, x.dtype, dev, x)
         for name, wanted in (("grad_weight", grad_weight), ("grad_bias", grad_bias)):
             if wanted:
-                res[name] = _out(out, name, (H,), x.dtype, dev)
+                res[name] = _out(out, name, (H,), x.dtype, dev, weight)
         ws = _workspace(n.value if grad_weight or grad_bias else 0, dev, workspace)
         _abi.check(L.plp_layer_norm_bwd(_ptr(grad_y), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), N, H, dt,
                                         1 if rms else 0, _ptr(res.get("grad_x")), _ptr(res.get("grad_weight")),
