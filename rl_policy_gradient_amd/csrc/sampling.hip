@@ -82,10 +82,11 @@ __device__ __forceinline__ double lane_of(double v, int l) {
   return __longlong_as_double((long long)lane_of((u64)__double_as_longlong(v), l));
 }
 // The value of another lane by a lane permutation (no LDS round trip); 0 where
-// it has no source or the row is not in ROWS.
+// it has no source or the row is not in ROWS (with all rows, the permutation
+// itself fills in the 0).
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int permuted(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, ROWS == 0xf);
 }
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t permuted(uint32_t v) {
@@ -202,41 +203,45 @@ __device__ __forceinline__ double rate_of(float tau) { return tau == 0.f ? 1.0 :
 
 // ---------------------------------------------------------------------------
 // First launch: per block of 256 its maximum (NaN if it holds one) and
-// sum exp((z - maximum) / tau), one block per half wave.
+// sum exp((z - maximum) / tau), one block per 16 lanes.
 // ---------------------------------------------------------------------------
 constexpr int kStatThreads = 256;
-constexpr int kStatBlocks = kStatThreads / kLanes;
+constexpr int kStatLanes = 16;                     // a row of lanes a block
+constexpr int kStatChunks = kLanes / kStatLanes;   // chunks a lane takes
+constexpr int kStatBlocks = kStatThreads / kStatLanes;
 
 // The larger, NaN if either is.
 struct MaxOrNan {
   __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
 };
 
-// Each half wave takes `rounds` blocks, kStatBlocks apart, the next one's
-// loads issued before the present one's arithmetic.
+// Every 16 lanes take `rounds` blocks, kStatBlocks apart.
 template <typename T>
 __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a, int G, int rounds) {
   const int64_t row = blockIdx.y;
   const Row<T> r(a, row);
-  const int nb = r.blocks(), lane = threadIdx.x % kLanes;
+  const int nb = r.blocks(), lane = threadIdx.x % kStatLanes;
   const float tau = temperature_of(a, row);
   const double rate = rate_of(tau), least = least_of(tau);
-  int b = blockIdx.x * rounds * kStatBlocks + threadIdx.x / kLanes;
-  float z[kChunk], next[kChunk];
-  if (b < nb) r.load(b * kLanes + lane, next);
-  for (int i = 0; i < rounds && b < nb; ++i, b += kStatBlocks) {  // uniform over the half wave
+  int b = blockIdx.x * rounds * kStatBlocks + threadIdx.x / kStatLanes;
+#pragma unroll 1
+  for (int i = 0; i < rounds && b < nb; ++i, b += kStatBlocks) {  // uniform over the 16 lanes
+    float z[kStatChunks][kChunk];
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) z[k] = next[k];
-    if (i + 1 < rounds && b + kStatBlocks < nb) r.load((b + kStatBlocks) * kLanes + lane, next);
-    float m = z[0];
+    for (int c = 0; c < kStatChunks; ++c) r.load(b * kLanes + c * kStatLanes + lane, z[c]);
+    float m = z[0][0];
 #pragma unroll
-    for (int k = 1; k < kChunk; ++k) m = MaxOrNan()(m, z[k]);
-    m = half_reduce(m, MaxOrNan());
+    for (int c = 0; c < kStatChunks; ++c)
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) m = MaxOrNan()(m, z[c][k]);
+    m = row_reduce(m, MaxOrNan());
     const double ref = m == -INFINITY ? 0.0 : (double)m;
     double s = 0.0;
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) s += exp2_of(fmax((double)z[k] - ref, least), rate);
-    s = half_reduce(s, Add());
+    for (int c = 0; c < kStatChunks; ++c)
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) s += exp2_of(fmax((double)z[c][k] - ref, least), rate);
+    s = row_reduce(s, Add());
     if (lane == 0) {
       a.block_max[row * G + b] = m;
       a.block_sum[row * G + b] = s;
