@@ -20,6 +20,16 @@
 // Two launches: the first reads the logits once and leaves each block of 256
 // its maximum and sum; the second, a workgroup a row, finds the cut and the
 // token from those and from the blocks that matter.
+//
+// What bounds them. The first: 16 operations in fp64 a logit, which one SIMD
+// issues at 2.2 ns a wave (fp32: 1.3), and the bytes, about evenly: 512 rows
+// of 151936 in fp32 take 68 us, of which the fp64 alone would be 42 and a copy
+// of their 311 MB takes 58. The second: the length of one row's chain of
+// steps on one CU, 6 us without limits, 14 where the maxima bound the cut
+// (1 row of 151936 bf16, top_k 50), 30 to 60 where the row is flat and read
+// once more. Both together: 1 row 17.5 us, 64 unlimited rows of 151936 bf16
+// 16.7, 128 flat rows of 32000 at top_p 0.9 45, 512 rows of 151936 fp32 with
+// settings of their own 142 (two rounds of rows on 256 CUs).
 #include "ops.h"
 
 #include <math.h>
@@ -173,26 +183,24 @@ struct Row {
   __device__ int chunks() const { return (V + lead + kChunk - 1) / kChunk; }
   __device__ int blocks() const { return (V + lead + kSampleBlock - 1) / kSampleBlock; }
   __device__ int first(int c) const { return c * kChunk - lead; }
-  __device__ __forceinline__ void load(int c, float (&z)[kChunk]) const {
+  // A chunk as it lies in memory: nothing waits for the load before `values`.
+  struct Raw {
+    uint4 w[kChunk * sizeof(T) / 16];
+  };
+  __device__ __forceinline__ Raw fetch(int c) const {
     const int e0 = first(c);
-    if (e0 >= 0 && e0 + kChunk <= V) {
-      if constexpr (sizeof(T) == 4) {
-        const float4 u = *(const float4*)(p + e0), v = *(const float4*)(p + e0 + 4);
-        z[0] = u.x, z[1] = u.y, z[2] = u.z, z[3] = u.w, z[4] = v.x, z[5] = v.y, z[6] = v.z, z[7] = v.w;
-      } else {
-        const uint4 u = *(const uint4*)(p + e0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (e0 >= 0 && e0 + kChunk <= V) return *(const Raw*)(p + e0);
+    T t[kChunk];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          z[2 * k] = __uint_as_float(w[k] << 16);
-          z[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kChunk; ++k) z[k] = e0 + k >= 0 && e0 + k < V ? (float)p[e0 + k] : -INFINITY;
-    }
+    for (int k = 0; k < kChunk; ++k) t[k] = e0 + k >= 0 && e0 + k < V ? p[e0 + k] : (T)-INFINITY;
+    return __builtin_bit_cast(Raw, t);
   }
+  __device__ static __forceinline__ void values(const Raw& raw, float (&z)[kChunk]) {
+    const T(&t)[kChunk] = reinterpret_cast<const T(&)[kChunk]>(raw);
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) z[k] = (float)t[k];
+  }
+  __device__ __forceinline__ void load(int c, float (&z)[kChunk]) const { values(fetch(c), z); }
 };
 
 __device__ __forceinline__ float temperature_of(const SampleArgs& a, int64_t row) {
@@ -215,37 +223,34 @@ struct MaxOrNan {
   __device__ __forceinline__ float operator()(float a, float b) const { return __builtin_elementwise_maximum(a, b); }
 };
 
-// Every 16 lanes take `rounds` blocks, kStatBlocks apart.
 template <typename T>
-__global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a, int G, int rounds) {
+__global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a, int G) {
   const int64_t row = blockIdx.y;
   const Row<T> r(a, row);
   const int nb = r.blocks(), lane = threadIdx.x % kStatLanes;
   const float tau = temperature_of(a, row);
   const double rate = rate_of(tau), least = least_of(tau);
-  int b = blockIdx.x * rounds * kStatBlocks + threadIdx.x / kStatLanes;
-#pragma unroll 1
-  for (int i = 0; i < rounds && b < nb; ++i, b += kStatBlocks) {  // uniform over the 16 lanes
-    float z[kStatChunks][kChunk];
+  const int b = blockIdx.x * kStatBlocks + threadIdx.x / kStatLanes;
+  if (b >= nb) return;  // the same for the 16 lanes
+  float z[kStatChunks][kChunk];
 #pragma unroll
-    for (int c = 0; c < kStatChunks; ++c) r.load(b * kLanes + c * kStatLanes + lane, z[c]);
-    float m = z[0][0];
+  for (int c = 0; c < kStatChunks; ++c) r.load(b * kLanes + c * kStatLanes + lane, z[c]);
+  float m = z[0][0];
 #pragma unroll
-    for (int c = 0; c < kStatChunks; ++c)
+  for (int c = 0; c < kStatChunks; ++c)
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) m = MaxOrNan()(m, z[c][k]);
-    m = row_reduce(m, MaxOrNan());
-    const double ref = m == -INFINITY ? 0.0 : (double)m;
-    double s = 0.0;
+    for (int k = 0; k < kChunk; ++k) m = MaxOrNan()(m, z[c][k]);
+  m = row_reduce(m, MaxOrNan());
+  const double ref = m == -INFINITY ? 0.0 : (double)m;
+  double s = 0.0;
 #pragma unroll
-    for (int c = 0; c < kStatChunks; ++c)
+  for (int c = 0; c < kStatChunks; ++c)
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) s += exp2_of(fmax((double)z[c][k] - ref, least), rate);
-    s = row_reduce(s, Add());
-    if (lane == 0) {
-      a.block_max[row * G + b] = m;
-      a.block_sum[row * G + b] = s;
-    }
+    for (int k = 0; k < kChunk; ++k) s += exp2_of(fmax((double)z[c][k] - ref, least), rate);
+  s = row_reduce(s, Add());
+  if (lane == 0) {
+    a.block_max[row * G + b] = m;
+    a.block_sum[row * G + b] = s;
   }
 }
 
@@ -269,21 +274,33 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
 //     a pass, until it can be listed.
 //
 // In each case the decision is the same whole-number one. The kernel runs once
-// through most of its code, so that its size counts: loops over a lane's eight
-// logits are not unrolled and each step has one place in the code (unrolled
-// and inlined where used it was 91 KB, and a row took two to three times as
-// long, fetching it).
+// through most of its code, so that its size counts (45 KB): loops over a
+// lane's eight logits are not unrolled where it can be helped and each step has
+// one place in the code (unrolled and inlined where used it was 91 KB, and a
+// row took two to three times as long, fetching it).
 // ---------------------------------------------------------------------------
 constexpr int NT = 1024;
 constexpr int kWaves = NT / 64;
 constexpr int kBins = 2048;
 constexpr int kBinsPer = kBins / NT;
 constexpr int kList = 4096;        // logits that can be listed
-constexpr int kRanked = NT / 4;    // up to so many, every listed logit is compared with every other
-constexpr int kAll = 1536;         // logits up to which a whole row is listed for top_k
-constexpr int kDirect = 32;        // active blocks up to which top_p's candidates are listed without an estimate
-constexpr int kEstimate = 16384;   // logits of the estimate, at least
-constexpr int kAround = 1250;      // logits listed on either side of the estimated cut, three times its usual error
+// Up to so many, every listed logit is compared with every other, else the
+// cut is searched for by histograms (51 listed: 18 us a call against 22).
+constexpr int kRanked = NT / 4;
+// Logits up to which a whole row is listed for top_k, when the maxima do not
+// bound it, instead of an estimate (64 rows, k = 50 to 400: of 300, 24 us
+// against 26; of 1000, 21 to 25 against 18 to 33; of 1500, 24 against 20).
+constexpr int kAll = 1024;
+// Active blocks up to which top_p's candidates are listed without an estimate
+// (64 flat rows of 16 blocks: 30 us against 32, of 28 blocks 35 against 32;
+// peaked rows of 28 blocks 22 against 25).
+constexpr int kDirect = 32;
+// Logits of the estimate, at least (64 flat rows of 151936 in fp32: 86 us;
+// 4096 of them miss the cut too often, 202; 65536 cost more than they save, 89).
+constexpr int kEstimate = 16384;
+// Logits listed on either side of the estimated cut: three times its usual
+// error, and two such lists within kList.
+constexpr int kAround = 1250;
 
 // A logit's place in the order, the larger the earlier: its key, then its
 // index from the end.
@@ -464,57 +481,66 @@ struct RowSampler {
     begin_pass();
     u64 above = 0;
     const int lane = threadIdx.x % kLanes;
-    float z[kChunk], next[kChunk];
-    int b = 0, bnext = 0;
+    // the half wave's logits above, in the place of the list's masses, which come later
+    float* const some = reinterpret_cast<float*>(ls.q) + threadIdx.x / kLanes * kSampleBlock;
+    typename Row<T>::Raw next;
+    int i = (int)threadIdx.x / kLanes;
+    if (i < nact) next = r.fetch(act[i] * kLanes + lane);
 #pragma unroll 1
-    for (int i = (int)(threadIdx.x / kLanes) - step; i < nact; i += step) {  // one block ahead
-      if (i + step < nact) {
-        bnext = act[i + step];
-        r.load(bnext * kLanes + lane, next);
+    for (; i < nact; i += step) {
+      const int b = act[i];
+      float z[kChunk];
+      r.values(next, z);
+      if (i + step < nact) next = r.fetch(act[i + step] * kLanes + lane);  // on the way meanwhile
+      uint32_t listed = 0, over = 0;
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        listed |= (z[k] >= zl) & (z[k] < zh) ? 1u << k : 0u;
+        over |= z[k] >= zh ? 1u << k : 0u;
       }
-      if (i >= 0) {
-        uint32_t listed = 0;
+      // both counts in one scan
+      const uint32_t mine = (uint32_t)__popc(listed) | (uint32_t)__popc(over) << 16, upto = wave_scan(mine);
+      if (__ballot(listed != 0)) {  // one addition to the count a wave (a half at the end)
+        const int e0 = r.first(b * kLanes + lane);
+        const int last = 63 - __clzll((long long)__ballot(1));
+        uint32_t at = 0;
+        if ((int)(threadIdx.x & 63) == last) at = atomicAdd(&sh.n, upto & 0xffff);
+        at = lane_of(at, last) + ((upto - mine) & 0xffff);
 #pragma unroll
-        for (int k = 0; k < kChunk; ++k) listed |= (z[k] >= zl) & (z[k] < zh) ? 1u << k : 0u;
-        if (__ballot(listed != 0)) {  // one addition to the count a wave (a half at the end)
-          const int e0 = r.first(b * kLanes + lane);
-          const uint32_t mine = (uint32_t)__popc(listed), upto = wave_scan(mine);
-          const int last = 63 - __clzll((long long)__ballot(1));
-          uint32_t at = 0;
-          if ((int)(threadIdx.x & 63) == last) at = atomicAdd(&sh.n, upto);
-          at = lane_of(at, last) + upto - mine;
-#pragma unroll
-          for (int k = 0; k < kChunk; ++k)
-            if (listed >> k & 1) {
-              if (at < kList) ls.list[at] = place_of(Key<T>::of(z[k]), e0 + k);
-              ++at;
-            }
-        }
-        if (zh < INFINITY) {  // uniform
-          // those not above as -inf, which has no mass: nothing depends on a
-          // branch, and the eight chains overlap
-          u64 kept = 0, all = 0;
-          if (least > 0.0) {
-#pragma unroll
-            for (int k = 0; k < kChunk; ++k) {
-              const double w = weight(z[k] >= zh ? z[k] : -INFINITY);
-              const u64 q = quant(w);
-              all += q;
-              kept += w >= least ? q : 0;
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < kChunk; ++k) all += quant(weight(z[k] >= zh ? z[k] : -INFINITY));
-            kept = all;
+        for (int k = 0; k < kChunk; ++k)
+          if (listed >> k & 1) {
+            if (at < kList) ls.list[at] = place_of(Key<T>::of(z[k]), e0 + k);
+            ++at;
           }
-          above += all;
-          kept = half_reduce(kept, Add());
-          if (lane == 0) bq[b] = kept;
-        }
       }
+      if (zh < INFINITY) {  // uniform
+        // A weight costs some 20 operations in fp64 and few of the logits are
+        // above, so the block's are first put side by side: 64 rows of 151936
+        // bf16 at top_p 0.9 and temperature 1.2, 93 us with all eight weights
+        // of a lane, 75 so (fp32 rows so flat that most are above: 86 and 94).
+        const uint32_t lower = lane_of(upto, 31) >> 16, both = lane_of(upto, 63) >> 16;
+        const bool second = threadIdx.x & 32;
+        const int n = (int)(second ? both - lower : lower);
+        uint32_t at = ((upto - mine) >> 16) - (second ? lower : 0);
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) z[k] = next[k];
-      b = bnext;
+        for (int k = 0; k < kChunk; ++k)
+          if (over >> k & 1) some[at++] = z[k];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // read by other lanes of the wave
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        u64 kept = 0;
+#pragma unroll 1
+        for (int j = lane; j < n; j += kLanes) {
+          const double w = weight(some[j]);
+          const u64 q = quant(w);
+          above += q;
+          kept += w >= least ? q : 0;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        kept = half_reduce(kept, Add());
+        if (lane == 0) bq[b] = kept;
+      }
     }
     end_pass(above);
   }
@@ -555,11 +581,11 @@ struct RowSampler {
   }
 
   // The cut within the list of n places from hi to lo, above which lies the
-  // mass `above`: kept are
-  // the first k (k >= n: no limit) of those the mass before which is below p
-  // times the mass of the first k with k_on, else of everything. False if the
-  // cut is not in the list, unless `whole`: then all of it is kept. Adds the
-  // kept ones to bq; through: the mass up to and with the cut.
+  // mass `above`: kept are the first k (k >= n: no limit) of those the mass
+  // before which is below p times the mass of the first k with k_on, else of
+  // everything. False if the cut is not in the list, unless `whole`: then all
+  // of it is kept. Adds the kept ones to bq; through: the mass up to and with
+  // the cut.
   __device__ __forceinline__ bool cut_in_list(int n, u64 lo, u64 hi, u64 above, u64 k, bool k_on, float p, double mass,
                                               bool whole, u64& cut, u64& through) {
     u64 mine = 0, total;
@@ -777,10 +803,11 @@ struct RowSampler {
   }
 
   // Bounds zl (raised) and zh of a neighbourhood of the cut. By count: a zl
-  // that k logits surely reach, give or take four standard deviations of the
-  // sample. Else of the cut above which a mass of `t` of the row's lies, from a sample of the row in which the mass below the cut is
-  // counted from the bottom, where no single logit weighs much. Logits below
-  // zl are surely below the cut.
+  // that t logits reach, give or take four standard deviations of the sample
+  // (the list's count tells whether they do). Else of the cut above which a
+  // mass of `t` of the row's lies, from a sample of the row in which the mass
+  // below the cut is counted from the bottom, where no single logit weighs
+  // much. Logits below zl on entry are surely below the cut.
   __device__ __forceinline__ void estimate(bool by_count, u64 t, float& zl, float& zh) {
     const float scale = (float)kBins / (mf - zl), ratef = (float)rate;
     const int chunks = r.chunks(), step = max(1, chunks * kChunk / kEstimate);
@@ -882,7 +909,9 @@ struct RowSampler {
       // with every other logit at most (1 - p) S / (2 x their number), it holds
       from = fmaxf(all, (float)(m + log2((1.0 - (double)fmaxf(top_p, 0.f)) * S / (512.0 * nb)) / rate));
     }
-    // (a row none of whose blocks holds a 32nd is flat: the bound would not be far above `from`)
+    // A row none of whose blocks holds a 32nd is flat: the bound would not be
+    // far above `from` (64 flat rows of 32000 bf16: 42 us against 44; peaked
+    // ones pay 0.5 us for the look).
     const bool flat = !k_on && p_on && !peaked();
     if (flat) L = from;
     else if (k_on ? top_k <= nb : p_on) L = bound(lowest_max, k_on, top_k, goal, k_on ? all : from);
@@ -1107,10 +1136,8 @@ hipError_t sample(const SampleArgs& a, hipStream_t st) {
     if (a.kept_logp) b.kept_logp = a.kept_logp + r0;
     b.block_max = a.block_max + r0 * G;
     b.block_sum = a.block_sum + r0 * G;
-    // several blocks a half wave once that leaves enough workgroups for the chip
-    const int rounds = (int)std::max<int64_t>(1, std::min<int64_t>(4, b.N * G / (kStatBlocks * 2048)));
-    sample_stats_kernel<T><<<dim3((G + kStatBlocks * rounds - 1) / (kStatBlocks * rounds), (unsigned)b.N), kStatThreads,
-                             0, st>>>(b, G, rounds);
+    sample_stats_kernel<T>
+        <<<dim3((G + kStatBlocks - 1) / kStatBlocks, (unsigned)b.N), kStatThreads, 0, st>>>(b, G);
     if (hipError_t e = hipGetLastError()) return e;
     if (a.top_k_rows || a.top_p_rows || a.min_p_rows || (a.top_k > 0 && a.top_k < a.V) || a.top_p < 1.f || a.min_p > 0.f)
       sample_row_kernel<T, true><<<(unsigned)b.N, NT, shared_bytes(G) + sizeof(Lists), st>>>(b, G);
