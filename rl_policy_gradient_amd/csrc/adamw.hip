@@ -11,7 +11,11 @@
 // would step by m / eps.
 //
 // Every element is read once and written once; nothing is reused, so the
-// step is bound by HBM.
+// step is bound by HBM: at 151936 x 896 bf16 with a master copy 390 us with
+// 8-bit states (16 bytes an element, 5.6 TB/s) and 705 us with fp32 ones (28
+// bytes, 5.4 TB/s), where a plain copy of 2.2 GB takes 422 us. 145 tensors of
+// a small model (27 million elements, 8-bit states) take 97 us in three
+// launches; a copy of their 435 MB 84.
 #include "ops.h"
 
 #include <math.h>
@@ -187,8 +191,8 @@ __device__ __forceinline__ uint32_t encode(f32x4 x, Scale sc, bool positive) {
 // scale's maximum never leaves the wave. One block a wave and nothing
 // unrolled: with 38 registers eight waves run on a SIMD, and it is their
 // number that keeps the bytes in flight. At 151936 x 896 bf16 with 8-bit
-// states, 400 us (5.5 TB/s); with two blocks a wave (65 registers) 465 us,
-// with four (113) 475 us; with fp32 states 694, 709 and 710 us.
+// states, 390 to 400 us; with two blocks a wave (65 registers) 465 us, with
+// four (113) 475 us; with fp32 states 694, 709 and 710 us.
 static_assert(kAdamBlock == 4 * 64 && kAdamTile == 4 * NT, "one block of a scale a wave, one tile a workgroup");
 
 template <typename P, typename G, bool MASTER, bool BITS8>

@@ -9,6 +9,15 @@
 //
 // The deviations are taken from the mean in a second pass over the row, so a
 // mean that is large beside them costs no precision.
+//
+// Bound by HBM: x is read once and y written once forward; x and dy are read
+// and dx written once backward, dw and db adding their partial rows. Measured:
+// forward of 65536 x 896 bf16 36 us (6.5 TB/s, cached in part; a copy of as
+// many bytes 33), of 16384 x 4096 fp32 101 us (5.3 TB/s); backward of 16384 x
+// 4096 fp32 151 us (5.3 TB/s; a copy of as many bytes 163), of 65536 x 896
+// bf16 72 us (4.9 TB/s), of 512 x 896 bf16 8 us, two launches of 5 and 3. Rows
+// that are no whole number of 16 bytes cost a third more: 65536 x 897 bf16 47
+// and 101 us.
 #include "ops.h"
 
 #include <algorithm>
@@ -40,10 +49,11 @@ __device__ float block_sum(float v, float* red) {
 // Rows of up to 16384: the row stays in registers, 16 elements a lane, and
 // LPR lanes share a row: 8 .. 128, powers of two, in a workgroup of 256 that
 // takes 256 / LPR rows at a time, or a workgroup of 192 .. 1024 a row (the
-// least that hold it), so that no row leaves many lanes idle. A lane loads 16 bytes at a time, whatever the row's alignment
-// (global loads and stores need only that of their elements); the row's last
-// few elements are the end of its last 16 bytes, and are stored 8, 4 and 2
-// bytes at a time.
+// least that hold it), so that no row leaves many lanes idle. A lane loads 16
+// bytes at a time, whatever the row's alignment (global loads and stores need
+// only that of their elements); the row's last few elements are the end of its
+// last 16 bytes, and are stored 8, 4 and 2 bytes at a time (65536 x 897 bf16:
+// 47 us forward and 101 backward, where an element at a time took 96 and 449).
 // ---------------------------------------------------------------------------
 constexpr int kPerLane = 16;
 constexpr int kMaxLanes = 1024;
@@ -212,8 +222,9 @@ __global__ __launch_bounds__(threads_of<LPR>) void norm_fwd_kernel(NormFwd a) {
 // dw and db in registers, then over its rows in LDS: one partial row each a
 // workgroup, added up by norm_bwd_reduce_kernel. What lies past H has x, dy and
 // w of 0 and adds nothing.
-// (bf16 rows are half as many bytes, so it takes four waves a SIMD rather
-// than three to keep enough in flight: 65536 x 896, 79 us against 105.)
+// (bf16 rows are half as many bytes, so it takes four waves a SIMD to keep
+// enough in flight where their tail costs registers: 16384 x 4100, 128 us
+// against 191; 65536 x 896 is at 72 either way.)
 template <typename T, int LPR, bool TAIL>
 __global__ __launch_bounds__(threads_of<LPR>, sizeof(T) == 4 ? 1 : 4) void norm_bwd_kernel(NormBwd a) {
   constexpr int slots = threads_of<LPR> / LPR, V = vec_of<T>;
@@ -466,8 +477,8 @@ hipError_t norm_bwd(const NormBwd& a, hipStream_t st) {
 }  // namespace
 
 // More groups hide more latency, fewer leave less to add up at the end: 768
-// where several rows share a workgroup, else 512 (65536 x 896 bf16: 78 us with
-// 512, 72 with 768, 75 with 1024; 16384 x 4096 fp32: 157, 162 and 165 us).
+// where several rows share a workgroup, else 512 (65536 x 896 bf16: 79 us with
+// 512, 72 with 768, 76 with 1024; 16384 x 4096 fp32: 155, 162 and 165 us).
 // The partial sums stay below 32 MB however long the row.
 int norm_bwd_groups(int64_t N, int H) {
   const int lanes = lanes_of(H), slots = lanes < NT ? NT / lanes : 1;

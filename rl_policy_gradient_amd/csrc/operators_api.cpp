@@ -75,7 +75,8 @@ int check_adamw_tensor(const plp_adamw_tensor& t, int i) {
            {t.exp_avg_scale, sb}, {t.exp_avg_sq_scale, sb}, {t.grad, n * ge}};
   for (int x = 0; x < 7; ++x)
     for (int y = 0; y < x; ++y)
-      if (overlap(r[x].p, r[x].n, r[y].p, r[y].n)) return fail(PLP_E_INVALID, "tensor %d: two of its arrays overlap", i);
+      if (overlap(r[x].p, r[x].n, r[y].p, r[y].n))
+        return fail(PLP_E_INVALID, "tensor %d: two of its arrays overlap", i);
   return PLP_OK;
 }
 
