@@ -29,7 +29,7 @@
 // (1 row of 151936 bf16, top_k 50), 30 to 60 where the row is flat and read
 // once more. Both together: 1 row 17.5 us, 64 unlimited rows of 151936 bf16
 // 16.7, 128 flat rows of 32000 at top_p 0.9 45, 512 rows of 151936 fp32 with
-// settings of their own 142 (two rounds of rows on 256 CUs).
+// settings of their own 142 to 160 (two rounds of rows on 256 CUs).
 #include "ops.h"
 
 #include <math.h>
