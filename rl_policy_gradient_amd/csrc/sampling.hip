@@ -292,15 +292,18 @@ constexpr int kRanked = NT / 4;
 // against 26; of 1000, 21 to 25 against 18 to 33; of 1500, 24 against 20).
 constexpr int kAll = 1024;
 // Active blocks up to which top_p's candidates are listed without an estimate
-// (64 flat rows of 16 blocks: 30 us against 32, of 28 blocks 35 against 32;
-// peaked rows of 28 blocks 22 against 25).
-constexpr int kDirect = 32;
+// in rows that are not flat (64 peaked rows of 32000 bf16 at top_p 0.9, 125
+// blocks: 25 us against 30; of 151936 with some 200 active, 35 against 40,
+// with nearly all 594 active 85 against 58).
+constexpr int kDirect = 256;
 // Logits of the estimate, at least (64 flat rows of 151936 in fp32: 86 us;
 // 4096 of them miss the cut too often, 202; 65536 cost more than they save, 89).
 constexpr int kEstimate = 16384;
-// Logits listed on either side of the estimated cut: three times its usual
-// error, and two such lists within kList.
-constexpr int kAround = 1250;
+// Logits listed on either side of the estimated cut: a margin for the bins'
+// own error, and kAround sqrt(V (step - 1)) for that of a sample of every
+// step-th, about three times its usual one (1250 of 151936; rows of 32000 are
+// sampled whole: 37 us instead of 42 with a list of 1250 either side).
+constexpr float kMargin = 32.f, kAround = 1.09f;
 
 // A logit's place in the order, the larger the earlier: its key, then its
 // index from the end.
@@ -443,10 +446,12 @@ struct RowSampler {
     return bin < 0 ? none : value(bin);
   }
 
-  // Whether a block holds a 32nd of the row's mass.
+  // Whether a block holds a 32nd of the row's mass, and four times its even
+  // share or half of everything.
   __device__ __forceinline__ bool peaked() {
     bool yes = false;
-    for (int b = threadIdx.x; b < nb; b += NT) yes |= __longlong_as_double((long long)bq[b]) * 32.0 >= S;
+    const double most = S * fmax(1.0 / 32.0, fmin(4.0 / (double)nb, 0.5));
+    for (int b = threadIdx.x; b < nb; b += NT) yes |= __longlong_as_double((long long)bq[b]) >= most;
     return __syncthreads_or(yes ? 1 : 0) != 0;
   }
 
@@ -879,8 +884,8 @@ struct RowSampler {
     if (threadIdx.x == 0 && (all >> 20) < 1u << 30) sh.bin_count = (uint32_t)all & 0xfffff;
     uint32_t at;
     __syncthreads();
-    // edges: kAround logits below the cut's bin and above it
-    const int around = kAround / step;
+    // edges: so many of the sample below the cut's bin and above it
+    const int around = (int)((kMargin + kAround * sqrtf((float)r.V * (float)(step - 1))) / (float)step);
     const int lo_at = (int)sh.bin_count - around, hi_at = (int)(sh.bin_count + ls.count[sh.bin]) + around;
     at = c0;
 #pragma unroll
@@ -909,9 +914,9 @@ struct RowSampler {
       // with every other logit at most (1 - p) S / (2 x their number), it holds
       from = fmaxf(all, (float)(m + log2((1.0 - (double)fmaxf(top_p, 0.f)) * S / (512.0 * nb)) / rate));
     }
-    // A row none of whose blocks holds a 32nd is flat: the bound would not be
-    // far above `from` (64 flat rows of 32000 bf16: 42 us against 44; peaked
-    // ones pay 0.5 us for the look).
+    // In a flat row the bound would not be far above `from`, and the list too
+    // long (64 flat rows of 32000 bf16: 37 us against 39 with a bound; of 4000,
+    // 21 against 30 when listed; peaked ones pay 0.5 us for the look).
     const bool flat = !k_on && p_on && !peaked();
     if (flat) L = from;
     else if (k_on ? top_k <= nb : p_on) L = bound(lowest_max, k_on, top_k, goal, k_on ? all : from);
@@ -939,7 +944,7 @@ struct RowSampler {
     const bool limits = k_on || p_on;
     // 0: list all candidates; 1: those around an estimate of the cut; 2: narrow
 #pragma unroll 1
-    for (int method = known && (k_on || !limits || nact <= kDirect || !(L < mf)) ? 0 : 1; method < 3; ++method) {
+    for (int method = known && (k_on || !limits || (nact <= kDirect && !flat) || !(L < mf)) ? 0 : 1; method < 3; ++method) {
       if (method == 1 && (k_on ? top_k > kList / 2 : !(L < mf))) continue;
       u64 lo = place, hi = top, an = 0;
       bool one_limit = false;  // k's cut first, then top_p's
