@@ -26,10 +26,10 @@
 // of 151936 in fp32 take 68 us, of which the fp64 alone would be 42 and a copy
 // of their 311 MB takes 58. The second: the length of one row's chain of
 // steps on one CU, 6 us without limits, 14 where the maxima bound the cut
-// (1 row of 151936 bf16, top_k 50), 30 to 60 where the row is flat and read
-// once more. Both together: 1 row 17.5 us, 64 unlimited rows of 151936 bf16
-// 16.7, 128 flat rows of 32000 at top_p 0.9 45, 512 rows of 151936 fp32 with
-// settings of their own 142 to 160 (two rounds of rows on 256 CUs).
+// (1 row of 151936 bf16, top_k 50), 30 to 70 where the row is flat and read
+// twice more. Both together: 1 row 17.6 us, 64 unlimited rows of 151936 bf16
+// 16.6, 128 flat rows of 32000 at top_p 0.9 39, 512 rows of 151936 fp32 with
+// settings of their own 142 to 171 (two rounds of rows on 256 CUs).
 #include "ops.h"
 
 #include <math.h>
@@ -266,9 +266,10 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
 //     before it give the cut (a few), or a radix search over their places in
 //     the order does (many).
 //  3. Where the maxima give no bound (fewer blocks than k) or the candidates
-//     are too many to list (top_p on a flat row), a histogram of about 16384
-//     logits of the row tells near which value the cut lies; one pass adds up
-//     what is above that neighbourhood and lists what is in it.
+//     are too many to list (top_p on a flat row, or many active blocks), a
+//     histogram of at least 16384 logits of the row tells near which value the
+//     cut lies; one pass adds up what is above that neighbourhood and lists
+//     what is in it.
 //  4. Where that fails too (a large k, thousands of equal logits at the cut),
 //     the neighbourhood is narrowed by exact histograms over places, 11 bits
 //     a pass, until it can be listed.
