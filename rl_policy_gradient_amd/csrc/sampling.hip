@@ -297,8 +297,8 @@ constexpr int kAll = 1024;
 // blocks: 25 us against 30; of 151936 with some 200 active, 35 against 40,
 // with nearly all 594 active 85 against 58).
 constexpr int kDirect = 256;
-// Logits of the estimate, at least (64 flat rows of 151936 in fp32: 86 us;
-// 4096 of them miss the cut too often, 202; 65536 cost more than they save, 89).
+// Logits of the estimate, at least (64 flat rows of 151936 in fp32: 94 us;
+// 8192 of them miss the cut too often, 210; 32768 cost what they save, 97).
 constexpr int kEstimate = 16384;
 // Logits listed on either side of the estimated cut: a margin for the bins'
 // own error, and kAround sqrt(V (step - 1)) for that of a sample of every
