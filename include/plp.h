@@ -418,8 +418,9 @@ typedef struct plp_sample_args {
  * top_p of those the ones before which the mass is below top_p times theirs
  * (so at least one), min_p those with w_i >= min_p. The token is the first, by
  * index, at which the running sum of the kept weights exceeds u times their
- * sum. Weights are formed in 64 bits and added exactly, so a row's result
- * depends on that row alone. temperature 0 takes the first of the largest
+ * sum. Weights are formed in 64 bits, rounded to 2^-50 of their sum or finer
+ * (less than half of that counts as nothing) and added exactly, so a row's
+ * result depends on that row alone. temperature 0 takes the first of the largest
  * logits and gives both log-probs as 0. A row that has no distribution (a
  * NaN, +inf, nothing above -inf; a setting or uniform that is NaN, a negative
  * or infinite temperature) gets token -1 and NaN log-probs. Uniforms outside

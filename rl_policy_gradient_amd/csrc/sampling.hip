@@ -958,7 +958,9 @@ struct RowSampler {
         }
         pass(nact, zl, zh);
         if (!limits) return place;
-        lo = last_place(max(lowest, Key<T>::of(zl)));  // at or below every place listed
+        // the last place of what is listed: of the least value that is not below zl
+        const uint32_t key = Key<T>::of(zl);
+        lo = last_place(max(lowest, key + (Key<T>::value(key) < zl)));
         if (zh < INFINITY) hi = last_place(Key<T>::of(zh)) | kIndexMask;  // at or above
         whole = whole && zl == L;
       } else {

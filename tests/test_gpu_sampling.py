@@ -374,3 +374,12 @@ def test_workspace_has_to_be_contiguous():
     z, u = (t.cuda() for t in logits(4, 100, "bf16", 1))
     with pytest.raises(ValueError, match="contiguous"):
         plp.sample_tokens(z, u, workspace=torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20))
+
+
+@pytest.mark.parametrize("V,k,tau,peaked", [(1697, 300, 1.0, False), (1797, 300, 2.5, True), (28755, 1000, 2.5, False)])
+def test_what_is_listed_ends_between_two_values(V, k, tau, peaked):
+    """Rows among which some list exactly k candidates above a bound that lies
+    between two neighbouring bf16 values: the lower one is not kept."""
+    require_gpu()
+    z, u = logits(340 if V > 10000 else 1000, V, "bf16", 7, peaked)
+    check(z, u, tau, k, 1.0, 0.0)
