@@ -275,7 +275,7 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
 //     a pass, until it can be listed.
 //
 // In each case the decision is the same whole-number one. The kernel runs once
-// through most of its code, so that its size counts (45 KB): loops over a
+// through most of its code, so that its size counts (36 KB): loops over a
 // lane's eight logits are not unrolled where it can be helped and each step has
 // one place in the code (unrolled and inlined where used it was 91 KB, and a
 // row took two to three times as long, fetching it).
