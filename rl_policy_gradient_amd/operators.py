@@ -10,6 +10,7 @@ include/plp.h, enqueued on the current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional, Sequence, Union
 
 import torch
@@ -190,14 +191,41 @@ def adamw_state(param: torch.Tensor, *, bits: int = 32, master: bool = False) ->
 
 
 class AdamWTable:
-    """A checked list of tensors for adamw_step, which keeps them alive. Build
-    it again when a tensor is replaced (a gradient newly allocated)."""
+    """A checked list of tensors for adamw_step. It holds the memory that its
+    pointers name, whatever becomes of the tensors. Build it again when a
+    tensor is replaced: a step refuses the table where a state's dict holds
+    another tensor or a parameter has other memory (.data, a checkpoint put
+    in its place). It does not see that there is a new gradient tensor, or
+    other memory behind a gradient or a state's tensor, and then goes on with
+    the ones it was given."""
 
-    def __init__(self, entries, tensors, device):
+    def __init__(self, entries, tensors, names, device):
         self.count = len(entries)
         self.device = device
         self.tensors = tensors
         self._array = (_abi.PlpAdamwTensor * max(1, self.count))(*entries)
+        self._params = [p for p, _, _ in tensors]
+        self._at = [p.data_ptr() for p in self._params]
+        # the states by name: what reads it, the dicts that have it, what they held
+        self._held = []
+        for k in dict.fromkeys(k for ks in names for k in ks):
+            dicts = [st for (_, _, st), ks in zip(tensors, names) if k in ks]
+            self._held.append((operator.itemgetter(k), dicts, [st[k] for st in dicts], k))
+        self._memory = [t.untyped_storage() for p, g, st in tensors for t in (p, g)]
+        self._memory += [t.untyped_storage() for _, _, held, _ in self._held for t in held]
+
+    def _check_current(self) -> None:
+        """A few microseconds for a dozen tensors: identities and pointers, in
+        one pass of C code each."""
+        for get, dicts, held, k in self._held:
+            try:
+                same = all(map(operator.is_, map(get, dicts), held))
+            except KeyError:
+                same = False
+            if not same:
+                raise ValueError(f"a state's {k!r} has been replaced since the table was built: build it again")
+        if list(map(torch.Tensor.data_ptr, self._params)) != self._at:
+            raise ValueError("a parameter has other memory than when the table was built: build it again")
 
 
 def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[dict], *,
@@ -214,7 +242,7 @@ def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], s
                                                                                               weight_decay]
     if len(decay) != len(params):
         raise ValueError(f"{len(decay)} weight decays for {len(params)} tensors")
-    entries, keep, ranges, dev = [], [], [], None
+    entries, keep, held, ranges, dev = [], [], [], [], None
     for i, (p, g, st, wd) in enumerate(zip(params, grads, states, decay)):
         bits = 8 if "exp_rms" in st else 32
         n = p.numel()
@@ -243,6 +271,7 @@ def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], s
         e.param_dtype, e.grad_dtype = _dtype_code(p), _dtype_code(g)
         entries.append(e)
         keep.append((p, g, st))
+        held.append(tuple(want))
         ranges += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{k} of tensor {i}", True)
                    for k, t in written.items() if t.numel()]
         ranges += [(g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), f"grad of tensor {i}", False)] * (n > 0)
@@ -255,7 +284,20 @@ def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], s
             end, who = b, name
         if w and b > end_w:
             end_w, who_w = b, name
-    return AdamWTable(entries, keep, dev)
+    return AdamWTable(entries, keep, held, dev)
+
+
+_ARGS_SIZE, _TENSOR_SIZE = ctypes.sizeof(_abi.PlpAdamwArgs), ctypes.sizeof(_abi.PlpAdamwTensor)
+
+
+def _on_device(t, dtype, name: str, table: AdamWTable) -> Optional[int]:
+    """The address of a step's scalar in device memory; None if it is none."""
+    if not isinstance(t, torch.Tensor):
+        return None
+    _check_vec(t, 1, dtype, name)
+    if table.device is not None and t.device != table.device:
+        raise ValueError(f"{name} is on {t.device}, the tensors on {table.device}")
+    return _ptr(t)
 
 
 def adamw_step(table: AdamWTable, *, lr: Union[float, torch.Tensor], step: Union[int, torch.Tensor],
@@ -265,24 +307,12 @@ def adamw_step(table: AdamWTable, *, lr: Union[float, torch.Tensor], step: Union
     read when the step runs, so that a captured graph can be replayed.
     grad_scale (fp32 [1] on the device) multiplies every gradient; where it is
     not finite the step changes nothing."""
-    a = _abi.PlpAdamwArgs()
-    a.struct_size, a.tensor_size = ctypes.sizeof(a), ctypes.sizeof(_abi.PlpAdamwTensor)
-    a.beta1, a.beta2, a.eps = float(betas[0]), float(betas[1]), float(eps)
-    scalars = {k: t for k, t in (("lr", lr), ("step", step), ("grad_scale", grad_scale)) if
-               isinstance(t, torch.Tensor)}
-    for name, t in scalars.items():
-        _check_vec(t, 1, torch.int64 if name == "step" else torch.float32, name)
-        if table.device is not None and t.device != table.device:
-            raise ValueError(f"{name} is on {t.device}, the tensors on {table.device}")
-    if "lr" in scalars:
-        a.lr_dev = _ptr(lr)
-    else:
-        a.lr = float(lr)
-    if "step" in scalars:
-        a.step_dev = _ptr(step)
-    else:
-        a.step = int(step)
-    a.grad_scale = _ptr(grad_scale)
+    table._check_current()
+    lr_at = _on_device(lr, torch.float32, "lr", table)
+    step_at = _on_device(step, torch.int64, "step", table)
+    scale_at = _on_device(grad_scale, torch.float32, "grad_scale", table)
+    a = _abi.PlpAdamwArgs(_ARGS_SIZE, _TENSOR_SIZE, float(lr) if lr_at is None else 0.0, float(betas[0]), float(betas[1]),
+                          float(eps), int(step) if step_at is None else 0, step_at, lr_at, scale_at)
     L = _abi.lib()
     if table.count == 0:
         _abi.check(L.plp_adamw_step(ctypes.byref(a), table._array, 0, None))
