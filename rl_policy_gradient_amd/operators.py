@@ -311,6 +311,8 @@ def adamw_step(table: AdamWTable, *, lr: Union[float, torch.Tensor], step: Union
     lr_at = _on_device(lr, torch.float32, "lr", table)
     step_at = _on_device(step, torch.int64, "step", table)
     scale_at = _on_device(grad_scale, torch.float32, "grad_scale", table)
+    if scale_at is None and grad_scale is not None:
+        raise ValueError(f"grad_scale: expected a tensor of one torch.float32, got {grad_scale!r}")
     a = _abi.PlpAdamwArgs(_ARGS_SIZE, _TENSOR_SIZE, float(lr) if lr_at is None else 0.0, float(betas[0]), float(betas[1]),
                           float(eps), int(step) if step_at is None else 0, step_at, lr_at, scale_at)
     L = _abi.lib()

@@ -102,3 +102,9 @@ def test_the_memory_of_every_pointer_is_held(plp):
     for t in later:
         a, b = t.data_ptr(), t.data_ptr() + t.numel()
         assert all(b <= at or a >= at + n for at, n in held)
+
+
+def test_a_scale_that_is_no_tensor_is_refused(plp):
+    _, _, _, table = make(plp)
+    with pytest.raises(ValueError, match="grad_scale"):
+        step(plp, table, grad_scale=0.5)
