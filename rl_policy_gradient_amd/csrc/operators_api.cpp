@@ -211,7 +211,7 @@ PLP_API int plp_adamw_step(const plp_adamw_args* a, const plp_adamw_tensor* tens
     d.ms = t.exp_avg_scale;
     d.vs = t.exp_avg_sq_scale;
     d.n = t.numel;
-    d.decay = a->lr_dev ? t.weight_decay : (float)(1.0 - a->lr * (double)t.weight_decay);
+    d.decay = a->lr_dev ? t.weight_decay : (float)(a->lr * (double)t.weight_decay);
     d.param_bf16 = t.param_dtype == PLP_DTYPE_BF16;
     d.grad_bf16 = t.grad_dtype == PLP_DTYPE_BF16;
     d.bits8 = t.state_bits == 8;

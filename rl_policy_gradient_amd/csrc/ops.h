@@ -44,7 +44,7 @@ struct AdamTensor {
   void* v;             // fp32 second moment, or e4m3 codes of its root
   float *ms, *vs;      // 8-bit states: one scale per kAdamBlock elements
   int64_t n;
-  float decay;         // 1 - lr weight_decay (weight_decay when the rate is read on the device)
+  float decay;         // lr weight_decay (weight_decay when the rate is read on the device)
   uint8_t param_bf16, grad_bf16, bits8;
 };
 constexpr int kAdamBlock = 256;   // elements of one scale
