@@ -9,6 +9,14 @@ import torch
 pytest.importorskip("rl_policy_gradient_amd._abi")
 
 
+@pytest.fixture(autouse=True)
+def float32_default():
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 class Launched(Exception):
     pass
 
