@@ -378,14 +378,24 @@ typedef struct plp_adamw_args {
  * returns), up to 52 of them a launch:
  *   g = grad_scale grad, m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps).
- * 8-bit states: each block of 256 elements is stored as the nearest e4m3 codes
- * (four significant bits, largest 448) under the scale max|x| / 448, after the
- * step has used the unrounded values; a root above zero keeps a code above
- * zero; an element that is not finite is stored as NaN (0x7f) and leaves its
- * block's scale alone. All-zero codes and scales are the initial state. Arrays
- * need the alignment of their elements; the arrays of one tensor must not
- * overlap (checked), nor those of different tensors (not checked). Errors:
- * PLP_E_INVALID, PLP_E_HIP. */
+ * 8-bit states: each block of 256 elements is stored as e4m3 codes (four
+ * significant bits, largest 448) under the scale max|x| / 448, after the step
+ * has used the unrounded values; a root above zero keeps a code above zero; an
+ * element that is not finite is stored as NaN (0x7f) and leaves its block's
+ * scale alone. A moment whose beta is at most 0.95 takes the nearest code. One
+ * with a larger beta would stay at its code, since a step changes it by less
+ * than half the distance to the next: it takes the code above or below, by the
+ * step's number and the element's place in its block alone, so that the mean
+ * over the steps is the value's own (so steps have to be numbered one after
+ * the other). Stored roots over fp32 ones, for noise of sizes a factor e apart
+ * in a block, mean and root mean square error: where sizes stay 1.00 and 8 %
+ * (beta2 0.95), 1.01 and 14 % (0.99), 1.01 and 15 % (0.999); where half of
+ * them fall to 0.03, after six times 1 / (1 - beta2) steps 0.97 and 28 %
+ * (0.99), 0.98 and 31 % (0.999); the nearest codes (0.95) follow later: 1.8
+ * after 119 steps, 1.1 after 200, 1.01 and 8 % after 300. All-zero codes and
+ * scales are the initial state. Arrays need the alignment of their elements;
+ * the arrays of one tensor must not overlap (checked), nor those of different
+ * tensors (not checked). Errors: PLP_E_INVALID, PLP_E_HIP. */
 PLP_API int plp_adamw_step(const plp_adamw_args* args, const plp_adamw_tensor* tensors, int32_t count,
                            hipStream_t stream);
 

@@ -172,8 +172,10 @@ def adamw_state(param: torch.Tensor, *, bits: int = 32, master: bool = False) ->
     """The state of one parameter before its first step. bits=32: "exp_avg"
     and "exp_avg_sq" in fp32; bits=8: "exp_avg" and "exp_rms" (the second
     moment's root) as float8_e4m3fn codes with an fp32 scale per 256 elements
-    in "exp_avg_scale" and "exp_rms_scale". master=True adds an fp32 copy of a
-    bfloat16 parameter, on which the step then works."""
+    in "exp_avg_scale" and "exp_rms_scale"; with a beta above 0.95 they are
+    right in the mean over steps numbered one after the other (plp_adamw_step).
+    master=True adds an fp32 copy of a bfloat16 parameter, on which the step
+    then works."""
     if bits not in (8, 32):
         raise ValueError(f"bits must be 8 or 32, got {bits}")
     new = lambda n, dt: torch.zeros(n, dtype=dt, device=param.device)  # noqa: E731
