@@ -246,8 +246,15 @@ __global__ __launch_bounds__(threads_of<LPR>, sizeof(T) == 4 ? 1 : 4) void norm_
     const float rstd = h ? a.rstd[at] : 0.f, mu = a.rms || !h ? 0.f : a.mean[at];
     float s = 0.f, q = 0.f;
 #pragma unroll
+    for (int e = 0; e < kPerLane; ++e) x[e] = (x[e] - mu) * rstd;
+    // past the row's end c is 0, but (0 - mu) rstd may be infinite where no
+    // element of the row's is (a row of one huge value)
+    if (!(fabsf(mu * rstd) < INFINITY)) {
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) x[e] = inside<V, LPR>(e, lane, H) ? x[e] : 0.f;
+    }
+#pragma unroll
     for (int e = 0; e < kPerLane; ++e) {
-      x[e] = (x[e] - mu) * rstd;
       const float c = gy[e] * w[e];
       s += c;
       q += c * x[e];
