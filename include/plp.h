@@ -429,8 +429,13 @@ typedef struct plp_sample_args {
  * (so at least one), min_p those with w_i >= min_p. The token is the first, by
  * index, at which the running sum of the kept weights exceeds u times their
  * sum. Weights are formed in 64 bits, rounded to 2^-50 of their sum or finer
- * (less than half of that counts as nothing) and added exactly, so a row's
- * result depends on that row alone. temperature 0 takes the first of the largest
+ * (less than half of that counts as nothing) and added exactly. Sums in 64
+ * bits, good to 1e-13 of themselves, are taken for the masses of blocks of 256
+ * logits where nothing limits the row, and for the whole mass that top_p
+ * without top_k refers to; their order goes by V and the row's address modulo
+ * 16 bytes. So a row's result does not depend on the other rows nor on its
+ * place among them, and on its address only where a border lies within that
+ * of u or top_p times the sum. temperature 0 takes the first of the largest
  * logits and gives both log-probs as 0. A row that has no distribution (a
  * NaN, +inf, nothing above -inf; a setting or uniform that is NaN, a negative
  * or infinite temperature) gets token -1 and NaN log-probs. Uniforms outside

@@ -9,10 +9,16 @@
 // equal to it. The token is the first index at which the kept weights' running
 // sum exceeds u times their sum.
 //
-// Every decision (which value is the cut, how many of it are kept, at which
-// index the sum is exceeded) is taken on whole numbers q_i = round(w_i 2^F),
-// F chosen so that they add up below 2^52: their sums are exact, so the
-// result does not depend on the order of additions or on the launch's shape.
+// What limits a row (which value is the cut, how many of it are kept) and at
+// which index the sum is exceeded is decided on whole numbers q_i =
+// round(w_i 2^F), F chosen so that they add up below 2^52: their sums are
+// exact, in whatever order. Two masses are sums in fp64 instead: a block's
+// where nothing limits the row, and the whole row's, of which top-p without
+// top-k keeps its part. They are added in a fixed order, which with the
+// blocks' bounds goes by the row's length and its address modulo 16 bytes, and
+// are good to 1e-13 of themselves (twice the exponential's 2e-14, and the
+// roundings of some 40 additions): a border that close to u or p times the
+// sum is all that a row's address can move.
 // w_i is formed in fp64 (2^x by its own polynomial, to 2e-14): at a vocabulary's
 // length an fp32 weight's rounding moves the running sum across a token of
 // the tail too often.
