@@ -997,14 +997,16 @@ struct RowSampler {
   }
 };
 
-// Bytes of LDS before the lists.
+// Bytes of LDS before the lists. Every part begins at a multiple of its
+// elements' size: the lists at one of 16, the blocks' 8-byte sums after Shared.
+static_assert(alignof(Lists) <= 16 && alignof(Shared) <= 16 && sizeof(Shared) % sizeof(u64) == 0, "LDS alignment");
 __host__ __device__ inline size_t shared_bytes(int G) {
   return (sizeof(Shared) + (size_t)G * (sizeof(u64) + sizeof(float) + sizeof(uint16_t)) + 15) / 16 * 16;
 }
 
 template <typename T, bool LIMITS>  // whether there may be any
 __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
-  extern __shared__ char lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // 8-byte members and atomics lie in it
   Shared& sh = *reinterpret_cast<Shared*>(lds);
   u64* bq = reinterpret_cast<u64*>(lds + sizeof(Shared));
   float* bmax = reinterpret_cast<float*>(bq + G);
