@@ -29,11 +29,12 @@
 // (Measured: 151936 x 896 bf16, 399 us with the nearest codes, 417 with these.)
 //
 // Every element is read once and written once; nothing is reused, so the
-// step is bound by HBM: at 151936 x 896 bf16 with a master copy 390 us with
-// 8-bit states (16 bytes an element, 5.6 TB/s) and 705 us with fp32 ones (28
-// bytes, 5.4 TB/s), where a plain copy of 2.2 GB takes 422 us. 145 tensors of
-// a small model (27 million elements, 8-bit states) take 97 us in three
-// launches; a copy of their 435 MB 84.
+// step is bound by HBM: at 151936 x 896 bf16 with a master copy 384 to 413 us
+// with 8-bit states (16 bytes an element, 5.3 to 5.7 TB/s; 363 to 488 under
+// the profiler) and 705 to 720 us with fp32 ones (28 bytes, 5.3 to 5.4 TB/s),
+// where a plain copy of 2.2 GB takes 422 us. 145 tensors of a small model (27
+// million elements, 8-bit states) take 97 to 101 us in three launches; a copy
+// of their 435 MB 84.
 #include "ops.h"
 
 #include <math.h>

@@ -12,12 +12,14 @@
 //
 // Bound by HBM: x is read once and y written once forward; x and dy are read
 // and dx written once backward, dw and db adding their partial rows. Measured:
-// forward of 65536 x 896 bf16 36 us (6.5 TB/s, cached in part; a copy of as
-// many bytes 33), of 16384 x 4096 fp32 101 us (5.3 TB/s); backward of 16384 x
-// 4096 fp32 151 us (5.3 TB/s; a copy of as many bytes 163), of 65536 x 896
-// bf16 72 us (4.9 TB/s), of 512 x 896 bf16 8 us, two launches of 5 and 3. Rows
-// that are no whole number of 16 bytes cost a third more: 65536 x 897 bf16 47
-// and 101 us.
+// forward of 65536 x 896 bf16 36 to 41 us (5.7 to 6.5 TB/s, cached in part; a
+// copy of as many bytes 33), of 16384 x 4096 fp32 101 us (5.3 TB/s); backward
+// of 16384 x 4096 fp32 150 to 154 us (5.2 to 5.4 TB/s; a copy of as many bytes
+// 163), of 65536 x 896 bf16 72 us (4.9 TB/s), of 512 x 896 bf16 8 us, two
+// launches of 5 and 3. Rows that are no whole number of 16 bytes cost a third
+// more or worse: 65536 x 897 bf16 47 and 100 us, backward of 16384 x 4099 fp32
+// 249; the widest of them (640 lanes and more) spill registers backward: 8192
+// x 12001 bf16 285 us, 4096 x 16383 153 where 16384 takes 92.
 #include "ops.h"
 
 #include <algorithm>

@@ -30,12 +30,17 @@
 // What bounds them. The first: 16 operations in fp64 a logit, which one SIMD
 // issues at 2.2 ns a wave (fp32: 1.3), and the bytes, about evenly: 512 rows
 // of 151936 in fp32 take 68 us, of which the fp64 alone would be 42 and a copy
-// of their 311 MB takes 58. The second: the length of one row's chain of
-// steps on one CU, 6 us without limits, 14 where the maxima bound the cut
-// (1 row of 151936 bf16, top_k 50), 30 to 70 where the row is flat and read
-// twice more. Both together: 1 row 17.6 us, 64 unlimited rows of 151936 bf16
-// 16.6, 128 flat rows of 32000 at top_p 0.9 39, 512 rows of 151936 fp32 with
-// settings of their own 142 to 171 (two rounds of rows on 256 CUs).
+// of their 311 MB takes 58. (64 rows of 151936 bf16 take 12, of which the fp64
+// is 5: their 9728 waves, a sixth more than run at once, have four blocks
+// each, taken together, and nothing to do while the loads are on the way.)
+// The second: the length of one row's chain of steps on one CU, 6 us without
+// limits, 14 where the maxima bound the cut (1 row of 151936 bf16, top_k 50),
+// 30 to 70 where the row is flat and read twice more; with limits it needs
+// all of a CU (128 registers, of which it spills 10 in fp32 and 4 in bf16, and
+// 16 waves that meet at every step). Both together: 1 row 17.6 to 18.1 us, 64
+// unlimited rows of 151936 bf16 15.7 to 16.6, 128 flat rows of 32000 at top_p
+// 0.9 39, 512 rows of 151936 fp32 with settings of their own 142 to 171 (two
+// rounds of rows on 256 CUs).
 #include "ops.h"
 
 #include <math.h>
