@@ -236,7 +236,9 @@ def adamw_table(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], s
     grads float32 or bfloat16 in any combination, states as adamw_state makes
     them (8 and 32 bits may be mixed), weight_decay one value or one per
     tensor. All are contiguous, on one GPU, and no two overlap but for
-    gradients, which are only read."""
+    gradients, which are only read. The checks take 6 to 8 microseconds a
+    tensor: meant for gradients in buffers that stay (out= of the calls that
+    give them), rather than a table a step."""
     params, grads, states = list(params), list(grads), list(states)
     if not len(params) == len(grads) == len(states):
         raise ValueError(f"{len(params)} params, {len(grads)} grads and {len(states)} states")
