@@ -15,8 +15,11 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libplp.so")
 BUILD = os.path.join(ROOT, "_build")
 
-SOURCES = ["lmhead_fwd.hip", "lmhead_fwd_o.hip", "lmhead_mfma.hip", "lmhead_generic.hip", "loss_stage.hip",
-           "plp_api.cpp", "layer_norm.hip", "adamw.hip", "sampling.hip", "operators_api.cpp"]
+# The fused path's own sources, then those of the operators around it: every
+# other file of csrc that is compiled by itself.
+FUSED = ["lmhead_fwd.hip", "lmhead_fwd_o.hip", "lmhead_mfma.hip", "lmhead_generic.hip", "loss_stage.hip",
+         "plp_api.cpp"]
+SOURCES = FUSED + sorted(f for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")) and f not in FUSED)
 
 # Per-source compiler options. Both two-role sweeps are faster without the
 # scheduler's unclustered high-register-pressure rescheduling stage (measured
