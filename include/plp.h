@@ -317,7 +317,8 @@ PLP_API int plp_policy_loss_from_logprobs(const plp_args* args, const float* log
 /* ---- Operators around the fused loss ---------------------------------------
  * The other calls of a policy's training loop: sampling the completions (the
  * targets and their old_logp), the final norm that gives `hidden` and takes
- * grad_hidden back, and the AdamW step that takes grad_weight and grad_bias.
+ * grad_hidden back, the AdamW step that takes grad_weight and grad_bias, the
+ * embedding and its gradient, and the norm of all gradients.
  * They follow the conventions above, but for alignment: a tensor needs only
  * the alignment of its elements. Outputs that share memory with an input or
  * with each other are refused (PLP_E_INVALID). These entry points were added
@@ -444,6 +445,58 @@ typedef struct plp_sample_args {
 PLP_API int plp_sample_tokens_workspace_size(int64_t N, int32_t V, size_t* bytes);
 PLP_API int plp_sample_tokens(const plp_sample_args* args, void* workspace, size_t workspace_bytes,
                               hipStream_t stream);
+
+/* Embedding lookup: y[n] = round(scale weight[tokens[n]]), a row of zeros where
+ * tokens[n] lies outside [0,V) (padding; the -1 of plp_sample_tokens). tokens
+ * [N] int64, weight [V,H] and y [N,H] of `dtype`; the product is formed in fp32.
+ * N = 0 does nothing. Errors: PLP_E_INVALID (sizes, NULLs, scale not finite,
+ * alignment, overlap), PLP_E_UNSUPPORTED (H > 65536), PLP_E_HIP. */
+PLP_API int plp_embedding_fwd(const int64_t* tokens, const void* weight, int64_t N, int32_t H, int32_t V, int32_t dtype,
+                              float scale, void* y, hipStream_t stream);
+
+/* Its gradient: grad_weight[v] = round(scale sum of grad_y[n] over tokens[n] = v),
+ * summed in fp32 in the order of n and then over parts of a token's rows in a
+ * fixed order, so results do not change from call to call. Tokens outside [0,V)
+ * give nothing. With `accumulate` nonzero the sum is added to what grad_weight
+ * holds (an embedding that shares the LM head's weight adds to the fused call's
+ * grad_weight), and rows without tokens are neither read nor written; without
+ * it they are set to zero. grad_y [N,H] of grad_y_dtype; grad_weight [V,H] of
+ * grad_weight_dtype: grad_y's, or fp32. N = 0 gives zeros, or with `accumulate`
+ * does nothing. Errors as above, and PLP_E_WORKSPACE; PLP_E_UNSUPPORTED for a
+ * bf16 grad_weight of an fp32 grad_y. */
+PLP_API int plp_embedding_bwd_workspace_size(int64_t N, int32_t H, int32_t V, int32_t grad_y_dtype, int32_t accumulate,
+                                             size_t* bytes);
+PLP_API int plp_embedding_bwd(const int64_t* tokens, const void* grad_y, int64_t N, int32_t H, int32_t V,
+                              int32_t grad_y_dtype, int32_t grad_weight_dtype, float scale, int32_t accumulate,
+                              void* grad_weight, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One tensor of plp_grad_norm and plp_clip_grads. */
+typedef struct plp_grad_tensor {
+  void* grad;                   /* [numel] dtype; may be NULL with numel 0 */
+  int64_t numel;                /* >= 0; of all tensors together at most 2^40 */
+  int32_t dtype;                /* plp_dtype */
+  int32_t pad0;
+} plp_grad_tensor;
+
+/* The global norm of `count` gradients (host array, read before the call
+ * returns; at most 2^20) and the factor that clips them, with s = grad_scale[0]
+ * (device; NULL: 1), a factor that the gradients still lack:
+ *   norm_out[0] = |s| sqrt(sum of g^2 over all tensors),
+ *   scale_out[0] = s min(1, max_norm / (norm + eps)), NaN where norm_out is not finite,
+ *   norms_out[i] = |s| sqrt(sum of g^2 over tensor i), NULL to skip.
+ * Squares are added in 64 bits in a fixed order. scale_out is what
+ * plp_adamw_step takes as grad_scale (NaN: that step changes nothing). max_norm:
+ * >= 0, infinity for no limit. A tensor listed twice counts twice. count = 0
+ * gives norm 0 and scale s. Errors: PLP_E_INVALID, PLP_E_WORKSPACE, PLP_E_HIP. */
+PLP_API int plp_grad_norm_workspace_size(const plp_grad_tensor* tensors, int32_t count, size_t* bytes);
+PLP_API int plp_grad_norm(const plp_grad_tensor* tensors, int32_t count, double max_norm, double eps,
+                          const float* grad_scale, float* norm_out, float* scale_out, float* norms_out, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* g = round(g scale[0]) in place over the same list, for optimizers that take no
+ * factor. A scale of 1, or one that is not finite, leaves every gradient as it
+ * is (unread). Tensors must not overlap each other (not checked). */
+PLP_API int plp_clip_grads(const plp_grad_tensor* tensors, int32_t count, const float* scale, hipStream_t stream);
 
 /* ---- Measurement helpers (not part of the method) -------------------------
  * Per-kernel timing of the two LM-head sweeps with HIP events recorded on the

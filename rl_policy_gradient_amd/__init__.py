@@ -17,6 +17,7 @@ import torch
 from . import _abi
 from ._abi import METRIC_NAMES, PlpError  # noqa: F401
 from ._marshal import _check_vec, _dtype_code, _ptr, _stream, _workspace
+from .gradients import GradTable, clip_grads, embedding_bwd, embedding_fwd, grad_norm, grad_table
 from .operators import (AdamWTable, adamw_state, adamw_step, adamw_table, layer_norm_bwd, layer_norm_fwd,
                         sample_tokens)
 
@@ -36,6 +37,12 @@ __all__ = [
     "adamw_table",
     "adamw_step",
     "AdamWTable",
+    "embedding_fwd",
+    "embedding_bwd",
+    "grad_table",
+    "grad_norm",
+    "clip_grads",
+    "GradTable",
     "METRIC_NAMES",
     "PlpError",
 ]

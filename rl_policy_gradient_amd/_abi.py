@@ -143,6 +143,15 @@ class PlpSampleArgs(ctypes.Structure):
     ]
 
 
+class PlpGradTensor(ctypes.Structure):
+    _fields_ = [
+        ("grad", _vp),
+        ("numel", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("pad0", ctypes.c_int32),
+    ]
+
+
 class PlpError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"plp error {code}: {msg}")
@@ -151,7 +160,9 @@ class PlpError(RuntimeError):
 
 # entry points added to ABI version 5 after its first libraries
 _LATER = ("plp_layer_norm_fwd", "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd",
-          "plp_adamw_step", "plp_sample_tokens_workspace_size", "plp_sample_tokens")
+          "plp_adamw_step", "plp_sample_tokens_workspace_size", "plp_sample_tokens",
+          "plp_embedding_fwd", "plp_embedding_bwd_workspace_size", "plp_embedding_bwd",
+          "plp_grad_norm_workspace_size", "plp_grad_norm", "plp_clip_grads")
 
 _lib = None
 
@@ -196,6 +207,12 @@ def lib() -> ctypes.CDLL:
     L.plp_adamw_step.argtypes = [P(PlpAdamwArgs), P(PlpAdamwTensor), i32, _vp]
     L.plp_sample_tokens_workspace_size.argtypes = [i64, i32, P(sz)]
     L.plp_sample_tokens.argtypes = [P(PlpSampleArgs), _vp, sz, _vp]
+    L.plp_embedding_fwd.argtypes = [_vp, _vp, i64, i32, i32, i32, ctypes.c_float, _vp, _vp]
+    L.plp_embedding_bwd_workspace_size.argtypes = [i64, i32, i32, i32, i32, P(sz)]
+    L.plp_embedding_bwd.argtypes = [_vp, _vp, i64, i32, i32, i32, i32, ctypes.c_float, i32, _vp, _vp, sz, _vp]
+    L.plp_grad_norm_workspace_size.argtypes = [P(PlpGradTensor), i32, P(sz)]
+    L.plp_grad_norm.argtypes = [P(PlpGradTensor), i32, f64, f64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+    L.plp_clip_grads.argtypes = [P(PlpGradTensor), i32, _vp, _vp]
     L.plp_profile_start.argtypes = [ctypes.c_int32]
     L.plp_profile_stop.argtypes = [P(ctypes.c_double), P(ctypes.c_int32)]
     L.plp_profile_stop_n.argtypes = [P(ctypes.c_double), P(ctypes.c_int32), ctypes.c_int32]
@@ -208,7 +225,8 @@ def lib() -> ctypes.CDLL:
                  "plp_entropy_quantile_mask_noalloc", "plp_prepared_weight_size", "plp_prepare_weight",
                  "plp_policy_loss_workspace_size", "plp_policy_loss_from_logprobs", "plp_layer_norm_fwd",
                  "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd", "plp_adamw_step", "plp_sample_tokens_workspace_size",
-                 "plp_sample_tokens"):
+                 "plp_sample_tokens", "plp_embedding_fwd", "plp_embedding_bwd_workspace_size", "plp_embedding_bwd",
+                 "plp_grad_norm_workspace_size", "plp_grad_norm", "plp_clip_grads"):
         getattr(L, name).restype = ctypes.c_int
     if L.plp_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI version {L.plp_abi_version()}, this binding {ABI_VERSION}: "

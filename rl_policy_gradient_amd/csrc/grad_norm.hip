@@ -1,0 +1,190 @@
+// The global norm of a list of gradients and the factor that clips them:
+//
+//   norm = |s| sqrt(sum over all tensors of g^2),
+//   scale = s min(1, max_norm / (norm + eps))         (NaN if norm is not finite)
+//
+// with s a given factor (1 without one), and the pass that applies a scale.
+//
+// Squares are formed and added in fp64: a square of an fp32 or bf16 value is
+// exact there (24 + 24 bits of 53) and neither over- nor underflows, so a norm
+// is good to half a step of fp32 whatever the gradients' size. Two launches: a
+// workgroup a tile leaves the tile's sum, then one workgroup adds the tiles'
+// sums in a fixed order (and others those of each tensor, where asked for).
+#include "training_ops.h"
+
+#include <math.h>
+
+namespace plp {
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int FT = 1024;  // threads that finish
+
+template <typename T>
+constexpr int vec_of = 16 / (int)sizeof(T);
+// 16 bytes of T at any element's address.
+template <typename T>
+struct Vec {
+  typedef T type __attribute__((ext_vector_type(vec_of<T>), aligned(sizeof(T))));
+};
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// The entry that workgroup b belongs to: the last that begins at or before it.
+__device__ __forceinline__ int entry_of(const GradLaunch& a, uint32_t b) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < (kGradMaxTensors + 63) / 64; ++i) {
+    const uint32_t e = i * 64 + (threadIdx.x & 63);
+    n += __popcll(__ballot(e < a.count && a.t[e < a.count ? e : 0].first <= b));
+  }
+  return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+// A workgroup's tile: elements [begin, begin + n) of entry e.
+struct Tile {
+  int e;
+  bool bf16;
+  int64_t begin, n;
+};
+__device__ __forceinline__ Tile tile_of(const GradLaunch& a, uint32_t b) {
+  Tile t;
+  t.e = entry_of(a, b);
+  const uint32_t first = a.t[t.e].first, tb = a.t[t.e].tail_bf16;
+  const uint32_t next = t.e + 1 < (int)a.count ? a.t[t.e + 1].first : a.groups;
+  t.bf16 = tb & 1;
+  t.begin = (int64_t)(b - first) << a.tile_shift;
+  t.n = b + 1 == next ? (int64_t)(tb >> 1) : (int64_t)1 << a.tile_shift;
+  return t;
+}
+
+template <typename T>
+__device__ __forceinline__ double squares(const T* p, int64_t n) {
+  typedef typename Vec<T>::type TV;
+  constexpr int V = vec_of<T>;
+  constexpr int64_t step = (int64_t)NT * V;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  const auto add = [&](const TV& x) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const double g = (double)(float)x[k];
+      s[k % 4] = fma(g, g, s[k % 4]);
+    }
+  };
+  int64_t i = (int64_t)threadIdx.x * V;
+  for (; i + 3 * step + V <= n; i += 4 * step) {
+    TV x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const TV*>(p + i + c * step);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) add(x[c]);
+  }
+  for (; i + V <= n; i += step) add(*reinterpret_cast<const TV*>(p + i));
+  for (; i < n; ++i) {  // fewer than V, of one thread
+    const double g = (double)(float)p[i];
+    s[0] = fma(g, g, s[0]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__global__ __launch_bounds__(NT) void grad_squares_kernel(const GradLaunch a, double* __restrict__ part,
+                                                          uint32_t* __restrict__ start) {
+  __shared__ double red[NT / 64];
+  const uint32_t b = blockIdx.x;
+  const Tile t = tile_of(a, b);
+  double s = t.bf16 ? squares((const __bf16*)a.t[t.e].p + t.begin, t.n) : squares((const float*)a.t[t.e].p + t.begin, t.n);
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    part[a.first_tile + b] = (red[0] + red[1]) + (red[2] + red[3]);
+    if (t.begin == 0) start[a.first_tensor + t.e] = a.first_tile + b;
+  }
+}
+
+// Workgroup 0 the whole norm, the others the tensors' norms, a wave each.
+__global__ __launch_bounds__(FT) void grad_finish_kernel(const GradFinish a) {
+  const double given = a.grad_scale ? (double)*a.grad_scale : 1.0;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (blockIdx.x > 0) {
+    const uint32_t i = (blockIdx.x - 1) * (FT / 64) + wave;
+    if (i >= a.count) return;
+    const uint32_t end = i + 1 < a.count ? a.start[i + 1] : a.tiles;
+    double s = 0.0;
+    for (uint32_t k = a.start[i] + lane; k < end; k += 64) s += a.part[k];
+    s = wave_sum(s);
+    if (lane == 0) a.norms[i] = (float)(fabs(given) * sqrt(s));
+    return;
+  }
+  __shared__ double red[FT / 64];
+  double s = 0.0;
+  for (uint32_t k = threadIdx.x; k < a.tiles; k += FT) s += a.part[k];
+  s = wave_sum(s);
+  if (lane == 0) red[wave] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int w = 0; w < FT / 64; ++w) s += red[w];
+    const double norm = fabs(given) * sqrt(s);
+    const float n32 = (float)norm;
+    a.norm[0] = n32;
+    a.scale[0] = fabsf(n32) < INFINITY ? (float)(given * fmin(1.0, a.max_norm / (norm + a.eps))) : NAN;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void clip(T* p, int64_t n, float f) {
+  typedef typename Vec<T>::type TV;
+  constexpr int V = vec_of<T>;
+  constexpr int64_t step = (int64_t)NT * V;
+  const auto scaled = [&](TV x) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = (T)((float)x[k] * f);
+    return x;
+  };
+  int64_t i = (int64_t)threadIdx.x * V;
+  for (; i + 3 * step + V <= n; i += 4 * step) {
+    TV x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const TV*>(p + i + c * step);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<TV*>(p + i + c * step) = scaled(x[c]);
+  }
+  for (; i + V <= n; i += step) *reinterpret_cast<TV*>(p + i) = scaled(*reinterpret_cast<const TV*>(p + i));
+  for (; i < n; ++i) p[i] = (T)((float)p[i] * f);
+}
+
+__global__ __launch_bounds__(NT) void grad_clip_kernel(const GradLaunch a, const float* __restrict__ scale) {
+  const float f = *scale;
+  if (f == 1.f || !(fabsf(f) < INFINITY)) return;
+  const Tile t = tile_of(a, blockIdx.x);
+  if (t.bf16)
+    clip((__bf16*)a.t[t.e].p + t.begin, t.n, f);
+  else
+    clip((float*)a.t[t.e].p + t.begin, t.n, f);
+}
+
+}  // namespace
+
+hipError_t launch_grad_squares(const GradLaunch& a, double* part, uint32_t* start, hipStream_t st) {
+  grad_squares_kernel<<<a.groups, NT, 0, st>>>(a, part, start);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_finish(const GradFinish& a, hipStream_t st) {
+  const uint32_t others = a.norms ? (a.count + FT / 64 - 1) / (FT / 64) : 0;
+  grad_finish_kernel<<<1 + others, FT, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const GradLaunch& a, const float* scale, hipStream_t st) {
+  grad_clip_kernel<<<a.groups, NT, 0, st>>>(a, scale);
+  return hipGetLastError();
+}
+
+}  // namespace plp

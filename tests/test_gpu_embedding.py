@@ -1,0 +1,306 @@
+"""The embedding and its gradient on the GPU against plain implementations.
+
+Forward: one product in fp32 and one rounding, bit for bit. Backward: sums in
+64 bits. A sum of n terms in fp32, in whatever parts, is off by at most n
+roundings of the sum of magnitudes; then come a product, an addition and the
+rounding to the gradient's type."""
+import pytest
+import torch
+
+from tests.gpu_helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(autouse=True)
+def float32_default():
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
+def tokens_of(kind, N, V, g):
+    if kind == "zipf":
+        t = (torch.rand(N, generator=g, dtype=torch.float64) * torch.log(torch.tensor(float(V + 1)))).exp().long()
+        return t.clamp(1, V) - 1
+    if kind == "same":
+        return torch.full((N,), V // 2)
+    if kind == "falling":
+        return (V - 1 - torch.arange(N)) % V
+    if kind == "none":
+        return torch.where(torch.rand(N, generator=g) < 0.5, -1, V + 3)
+    if kind == "padded":  # two in five hold no token, of every kind of value that is none
+        t = torch.randint(0, V, (N,), generator=g)
+        bad = torch.tensor([-1, -100, V, 2 ** 40, -2 ** 63, 2 ** 32])[torch.randint(0, 6, (N,), generator=g)]
+        return torch.where(torch.rand(N, generator=g) < 0.4, bad, t)
+    if kind == "heavy":  # two in five are one token
+        return torch.where(torch.rand(N, generator=g) < 0.4, V - 1, torch.randint(0, V, (N,), generator=g))
+    return torch.randint(0, V, (N,), generator=g)
+
+
+KINDS = ["zipf", "same", "falling", "none", "padded", "heavy", "uniform"]
+SIZES = [(1, 1, 1), (1, 5, 3), (2, 8, 2), (3, 512, 7), (63, 7, 1), (64, 64, 1000), (257, 33, 5), (511, 896, 3000),
+         (4096, 40, 1000), (4097, 40, 1000), (5000, 17, 200000), (20000, 72, 1500)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["zipf", "padded", "none"])
+@pytest.mark.parametrize("N,H,V", SIZES)
+def test_forward(N, H, V, kind, dtype):
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator().manual_seed(N + H)
+    w, t = torch.randn(V, H, generator=g).to(DT[dtype]), tokens_of(kind, N, V, g)
+    for scale in (1.0, 29.933259, -0.37):
+        y = plp.embedding_fwd(t.cuda(), w.cuda(), scale=scale)["y"].cpu()
+        inside = ((t >= 0) & (t < V))[:, None]
+        want = torch.where(inside, (w[t.clamp(0, V - 1)].float() * torch.tensor(scale)).to(w.dtype), 0.0)
+        assert y.dtype == w.dtype and torch.equal(y, want.to(w.dtype))
+
+
+def reference(t, gy, V, scale, old=None):
+    """Sums in 64 bits, and how far the kernel's may be off."""
+    H = gy.shape[1]
+    inside = (t >= 0) & (t < V)
+    ti, gi = t[inside], gy[inside].double()
+    s = torch.zeros(V, H, dtype=torch.float64).index_add_(0, ti, gi)
+    mag = torch.zeros(V, H, dtype=torch.float64).index_add_(0, ti, gi.abs())
+    n = torch.bincount(ti, minlength=V).double()[:, None]
+    scale = float(torch.tensor(scale, dtype=torch.float32))
+    want, off = scale * s, abs(scale) * mag * (n + 2) * U
+    if old is not None:
+        want = want + old.double()
+        off = off + (want.abs() + off) * U
+    return want, off, n[:, 0] > 0
+
+
+def check_bwd(t, gy, V, scale, gdt, accumulate, device_gy=None, old=None):
+    import rl_policy_gradient_amd as plp
+    kw = {}
+    if accumulate:
+        if old is None:
+            old = torch.randn(V, gy.shape[1], generator=torch.Generator().manual_seed(9)).to(gdt)
+        out = old.cuda()
+        kw = dict(accumulate=True, out={"grad_weight": out})
+    else:
+        out = torch.full((V, gy.shape[1]), float("nan"), dtype=gdt, device="cuda")
+        kw = dict(out={"grad_weight": out})
+    r = plp.embedding_bwd(gy.cuda() if device_gy is None else device_gy, t.cuda(), V, scale=scale, grad_dtype=gdt, **kw)
+    assert r["grad_weight"] is out
+    want, off, touched = reference(t, gy, V, scale, old if accumulate else None)
+    got = out.cpu()
+    bad = (got.double() - want).abs() > off + HALF[gdt] * (want.abs() + off)
+    assert not bad.any(), (bad.nonzero()[:3], got[bad][:3], want[bad][:3])
+    rest = got[~touched]
+    assert torch.equal(rest, old[~touched] if accumulate else torch.zeros_like(rest))
+    return got
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("N,H,V", SIZES)
+def test_backward(N, H, V, kind, accumulate, types):
+    require_gpu()
+    g = torch.Generator().manual_seed(31 * N + H)
+    gy = torch.randn(N, H, generator=g).to(DT[types[0]])
+    check_bwd(tokens_of(kind, N, V, g), gy, V, 1.0 if H % 2 else 3.3, DT[types[1]], accumulate)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", ["zipf", "heavy", "same", "falling"])
+@pytest.mark.parametrize("N,H,V", [(70001, 24, 151936), (300000, 9, 1 << 20), (262145, 16, 1023), (66000, 8, 3_000_000),
+                                   (9000, 1030, 40000)])
+def test_backward_of_many_tokens(N, H, V, kind, accumulate):
+    """Two and three passes of the sort, and rows whose tokens lie in thousands of ranges."""
+    require_gpu()
+    g = torch.Generator().manual_seed(N)
+    gy = torch.randn(N, H, generator=g).bfloat16()
+    check_bwd(tokens_of(kind, N, V, g), gy, V, 1.0, torch.float32, accumulate)
+
+
+def test_same_bits_at_every_call():
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator().manual_seed(4)
+    for N in (3000, 50000):
+        t, gy = tokens_of("heavy", N, 4000, g).cuda(), torch.randn(N, 100, generator=g).cuda()
+        first = plp.embedding_bwd(gy, t, 4000)["grad_weight"]
+        for _ in range(5):
+            assert torch.equal(plp.embedding_bwd(gy, t, 4000)["grad_weight"], first)
+
+
+@pytest.mark.parametrize("shift", [1, 3, 7])
+@pytest.mark.parametrize("H", [1, 6, 8, 65, 520])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_any_alignment(dtype, H, shift):
+    """Tensors that begin anywhere in memory; what lies around the outputs stays."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    N, V, dt = 300, 50, DT[dtype]
+    g = torch.Generator().manual_seed(H)
+
+    def placed(x):
+        buf = torch.full((x.numel() + 32,), 7.0, dtype=x.dtype, device="cuda")
+        view = buf[shift:shift + x.numel()].view(x.shape)
+        view.copy_(x)
+        return buf, view
+
+    t = tokens_of("padded", N, V, g)
+    w, gy, old = (torch.randn(n, H, generator=g).to(dt) for n in (V, N, V))
+    _, wd = placed(w)
+    buf, y = placed(torch.zeros(N, H, dtype=dt))
+    plp.embedding_fwd(t.cuda(), wd, scale=2.5, out={"y": y})
+    inside = ((t >= 0) & (t < V))[:, None]
+    assert torch.equal(y.cpu(), torch.where(inside, (w[t.clamp(0, V - 1)].float() * 2.5).to(dt), 0.0).to(dt))
+    assert (buf[:shift] == 7).all() and (buf[shift + y.numel():] == 7).all()
+    _, gyd = placed(gy)
+    for accumulate in (False, True):
+        buf, gw = placed(old)
+        plp.embedding_bwd(gyd, t.cuda(), V, accumulate=accumulate, out={"grad_weight": gw})
+        want, off, touched = reference(t, gy, V, 1.0, old if accumulate else None)
+        assert ((gw.cpu().double() - want).abs() <= off + HALF[dt] * (want.abs() + off)).all()
+        assert (buf[:shift] == 7).all() and (buf[shift + gw.numel():] == 7).all()
+
+
+def test_values_that_are_not_finite_stay_in_their_rows():
+    require_gpu()
+    g = torch.Generator().manual_seed(0)
+    N, H, V = 6000, 20, 300
+    import rl_policy_gradient_amd as plp
+    t, gy = torch.randint(0, V, (N,), generator=g), torch.randn(N, H, generator=g)
+    t[:4] = torch.tensor([5, 5, 9, -1])
+    gy[0, 3], gy[1, 3], gy[2, 4], gy[3] = float("inf"), float("-inf"), float("inf"), float("nan")
+    gw = plp.embedding_bwd(gy.cuda(), t.cuda(), V)["grad_weight"].cpu()
+    assert torch.isnan(gw[5, 3]) and gw[9, 4] == float("inf")
+    gw[5, 3] = gw[9, 4] = 0.0
+    assert torch.isfinite(gw).all()
+    old = torch.full((V, H), float("nan"), device="cuda")
+    plp.embedding_bwd(torch.ones(1, H).cuda(), torch.tensor([7]).cuda(), V, accumulate=True, out={"grad_weight": old})
+    assert torch.isnan(old).all()
+    old[7] = 1.0
+    plp.embedding_bwd(torch.ones(1, H).cuda(), torch.tensor([7]).cuda(), V, accumulate=True, out={"grad_weight": old})
+    assert (old[7] == 2).all() and torch.isnan(old[:7]).all() and torch.isnan(old[8:]).all()
+
+
+def test_no_tokens_and_shapes():
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    none = torch.zeros(0, dtype=torch.int64, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        w = torch.randn(5, 3, device="cuda").to(dt)
+        assert plp.embedding_fwd(none, w)["y"].shape == (0, 3)
+        for at in (0, 1):
+            buf = torch.ones(20, dtype=dt, device="cuda")
+            gw = buf[at:at + 15].view(5, 3)
+            plp.embedding_bwd(torch.zeros(0, 3, device="cuda", dtype=dt), none, 5, out={"grad_weight": gw})
+            assert (gw == 0).all() and (buf[:at] == 1).all() and (buf[at + 15:] == 1).all()
+            gw.fill_(2)
+            plp.embedding_bwd(torch.zeros(0, 3, device="cuda", dtype=dt), none, 5, accumulate=True,
+                              out={"grad_weight": gw})
+            assert (gw == 2).all()
+    t = torch.randint(0, 5, (2, 3, 4), device="cuda")
+    w = torch.randn(5, 6, device="cuda")
+    y = plp.embedding_fwd(t, w)["y"]
+    assert torch.equal(y, w[t])
+    one = plp.embedding_fwd(t[0, 0, 0].clone(), w)["y"]
+    assert torch.equal(one, w[t[0, 0, 0]])
+    gw = plp.embedding_bwd(y, t, 5)["grad_weight"]
+    assert torch.equal(gw, plp.embedding_bwd(y.view(24, 6), t.view(24), 5)["grad_weight"])
+
+
+def test_gradient_is_the_forwards():
+    """Against autograd of the formula in 64 bits, and against differences of the
+    forward pass along a direction (the map is linear: no step to choose)."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator().manual_seed(2)
+    N, H, V, scale = 700, 48, 90, 6.9282
+    t = tokens_of("padded", N, V, g)
+    w, c, d = torch.randn(V, H, generator=g), torch.randn(N, H, generator=g), torch.randn(V, H, generator=g)
+    gw = plp.embedding_bwd(c.cuda(), t.cuda(), V, scale=scale)["grad_weight"].cpu().double()
+    s32 = float(torch.tensor(scale, dtype=torch.float32))
+    leaf = w.double().requires_grad_()
+    inside = ((t >= 0) & (t < V))[:, None].double()
+    ((leaf[t.clamp(0, V - 1)] * inside * s32) * c.double()).sum().backward()
+    _, off, _ = reference(t, c, V, scale)
+    assert ((gw - leaf.grad).abs() <= off + U * leaf.grad.abs()).all()
+    y0, y1 = (plp.embedding_fwd(t.cuda(), x.cuda(), scale=scale)["y"].cpu().double() for x in (w, w + d))
+    diff, along = ((y1 - y0) * c.double()).sum(), (gw * ((w + d).double() - w.double())).sum()
+    # a rounding of each of the forward's values, and the gradient's own error
+    most = (U * (y0.abs() + y1.abs()) * c.double().abs()).sum() + ((off + U * gw.abs()) * d.double().abs() * 1.01).sum()
+    assert (diff - along).abs() <= most
+
+
+def test_tables_past_32_bits():
+    """More than 2^32 bytes and 2^31 elements in the table, its gradient and the rows."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    V, H = 70000, 32768
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    t = torch.tensor([V - 1, 3, 65536, V - 1, 40000], device="cuda")
+    for v in t.tolist():
+        w[v] = float(v % 251)
+    y = plp.embedding_fwd(t, w)["y"]
+    assert torch.equal(y, w[t])
+    plp.embedding_bwd(torch.ones_like(y), t, V, accumulate=True, out={"grad_weight": w})
+    assert (w[V - 1] == float((V - 1) % 251) + 2).all() and (w[65536] == 65536 % 251 + 1).all()
+    assert (w[V - 2] == 0).all()
+    w.fill_(5)
+    plp.embedding_bwd(torch.ones_like(y), t, V, out={"grad_weight": w})
+    assert (w[V - 1] == 2).all() and (w[40000] == 1).all() and w.double().sum().item() == 5.0 * H
+    del w, y
+    N, H = 70000, 32768
+    gy = torch.zeros(N, H, dtype=torch.bfloat16, device="cuda")
+    gy[N - 1], gy[0], gy[65536] = 1, 2, 4
+    t = torch.full((N,), 1, device="cuda")
+    t[N - 1], t[0] = 0, 0
+    gw = plp.embedding_bwd(gy, t, 3)["grad_weight"]
+    assert (gw[0] == 3).all() and (gw[1] == 4).all() and (gw[2] == 0).all()
+    y = plp.embedding_fwd(t, gw)["y"]
+    assert (y[N - 1] == 3).all() and (y[65536] == 4).all()
+
+
+def test_streams_and_graphs():
+    """On a stream of its own, and captured twice over separate memory and
+    replayed in turn between eager calls."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    N, H, V = 5000, 64, 800
+
+    def make(seed):
+        g = torch.Generator().manual_seed(seed)
+        return tokens_of("zipf", N, V, g).cuda(), torch.randn(V, H, generator=g).bfloat16().cuda()
+
+    def run(t, w):
+        y = plp.embedding_fwd(t, w, scale=2.0)["y"]
+        gw = plp.embedding_bwd(y, t, V, grad_dtype=torch.float32)["grad_weight"]
+        plp.embedding_bwd(y, t, V, accumulate=True, out={"grad_weight": gw}, grad_dtype=torch.float32)
+        return y, gw
+
+    graphs = []
+    for seed in (1, 2):
+        t, w = make(seed)
+        want = [x.clone() for x in run(t, w)]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = run(t, w)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run(t, w)
+        graphs.append((graph, out, t, w))
+    for i in range(4):
+        for graph, out, t, w in graphs:
+            t.copy_((t + 7 * i) % V)
+            w.mul_(1.25)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, run(t, w)))
