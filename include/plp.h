@@ -446,6 +446,60 @@ PLP_API int plp_sample_tokens_workspace_size(int64_t N, int32_t V, size_t* bytes
 PLP_API int plp_sample_tokens(const plp_sample_args* args, void* workspace, size_t workspace_bytes,
                               hipStream_t stream);
 
+/* How one side's rows of logits are sampled: as in plp_sample_args, one value
+ * for all sequences or one a sequence ([B] arrays, NULL: the value). */
+typedef struct plp_token_limits {
+  float temperature, top_p, min_p;
+  int32_t top_k;
+  const float* temperature_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+  const int32_t* top_k_rows;
+} plp_token_limits;
+
+/* Inputs and outputs of plp_verify_tokens. */
+typedef struct plp_verify_args {
+  uint32_t struct_size;         /* sizeof(plp_verify_args) */
+  int32_t dtype;                /* plp_dtype of both models' logits */
+  int64_t B;                    /* sequences, >= 0 */
+  int32_t K;                    /* drafted tokens a sequence, 0 .. 1024 */
+  int32_t V;                    /* vocabulary size, 1 .. 2^20 */
+  const void* logits;           /* [B,K+1,V] the target's: row k before draft k, row K after the last */
+  int64_t seq_stride, row_stride;             /* elements, >= 0; a row of V is contiguous */
+  const void* draft_logits;     /* [B,K,V] that the drafts were sampled from, or NULL: each is certain */
+  int64_t draft_seq_stride, draft_row_stride;
+  const int64_t* draft_tokens;  /* [B,K] */
+  const int32_t* num_drafts;    /* [B] drafts of each sequence, taken into [0,K]; NULL: K */
+  const float* uniforms;        /* [B,K+1] in [0,1): K for the drafts, the last for the token after them */
+  plp_token_limits target, draft;             /* draft is read with draft_logits only */
+  int64_t* tokens_out;          /* [B,K+1] the accepted drafts, one token more, then -1 */
+  int32_t* accepted_out;        /* [B] drafts accepted */
+  float* logp_out;              /* [B,K+1] or NULL: log-probs of the tokens as plp_sample_tokens gives */
+  float* kept_logp_out;         /*   them (logp, kept_logp), 0 after the last token */
+} plp_verify_args;
+
+/* Verification of drafted tokens. With p_k the distribution that
+ * plp_sample_tokens draws from in the target's row k and q_k that of the draft's
+ * row k under its own settings (1 at d_k where drafts are certain): draft d_k is
+ * accepted if u_k q_k(d_k) < p_k(d_k), as long as all before it are. The token
+ * after the last accepted one is drawn from max(0, p_k - q_k) where draft k was
+ * refused, and from p_n after all n of them were accepted: the first index at
+ * which the running sum exceeds the last uniform times the sum. Each token is
+ * then distributed as one drawn from p. (Where p_k - q_k is nowhere above
+ * zero, as for a draft that neither side could give, it is drawn from p_k.) A draft outside [0,V) is refused. Rows past
+ * the sequence's num_drafts are not read. Probabilities are formed in 64 bits,
+ * good to about 1e-13 of themselves (one below 2^-1000 of the row's largest is
+ * 0); sums in an order that goes by V, so a
+ * sequence's result does not depend on the others, and on its place in memory
+ * only where a border lies within that of a uniform. A sequence that comes to a
+ * row without a distribution (plp_sample_tokens says which; the target's, or the
+ * draft's of a draft that all before were accepted), or to a uniform that is
+ * NaN, ends there with token -1 and NaN log-probs. Uniforms outside [0,1) are
+ * taken as the nearest inside. B = 0 does nothing. Errors: PLP_E_INVALID,
+ * PLP_E_UNSUPPORTED (K > 1024, V > 2^20), PLP_E_WORKSPACE, PLP_E_HIP. */
+PLP_API int plp_verify_tokens_workspace_size(int64_t B, int32_t K, int32_t V, int32_t draft_logits, size_t* bytes);
+PLP_API int plp_verify_tokens(const plp_verify_args* args, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Embedding lookup: y[n] = round(scale weight[tokens[n]]), a row of zeros where
  * tokens[n] lies outside [0,V) (padding; the -1 of plp_sample_tokens). tokens
  * [N] int64, weight [V,H] and y [N,H] of `dtype`; the product is formed in fp32.

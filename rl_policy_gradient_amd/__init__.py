@@ -20,6 +20,7 @@ from ._marshal import _check_vec, _dtype_code, _ptr, _stream, _workspace
 from .gradients import GradTable, clip_grads, embedding_bwd, embedding_fwd, grad_norm, grad_table
 from .operators import (AdamWTable, adamw_state, adamw_step, adamw_table, layer_norm_bwd, layer_norm_fwd,
                         sample_tokens)
+from .verify import verify_tokens
 
 __all__ = [
     "fused_lmhead_policy_loss_fwd_bwd",
@@ -37,6 +38,7 @@ __all__ = [
     "adamw_table",
     "adamw_step",
     "AdamWTable",
+    "verify_tokens",
     "embedding_fwd",
     "embedding_bwd",
     "grad_table",

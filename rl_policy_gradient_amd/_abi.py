@@ -143,6 +143,44 @@ class PlpSampleArgs(ctypes.Structure):
     ]
 
 
+class PlpTokenLimits(ctypes.Structure):
+    _fields_ = [
+        ("temperature", ctypes.c_float),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
+        ("top_k", ctypes.c_int32),
+        ("temperature_rows", _vp),
+        ("top_p_rows", _vp),
+        ("min_p_rows", _vp),
+        ("top_k_rows", _vp),
+    ]
+
+
+class PlpVerifyArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32),
+        ("dtype", ctypes.c_int32),
+        ("B", ctypes.c_int64),
+        ("K", ctypes.c_int32),
+        ("V", ctypes.c_int32),
+        ("logits", _vp),
+        ("seq_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("draft_logits", _vp),
+        ("draft_seq_stride", ctypes.c_int64),
+        ("draft_row_stride", ctypes.c_int64),
+        ("draft_tokens", _vp),
+        ("num_drafts", _vp),
+        ("uniforms", _vp),
+        ("target", PlpTokenLimits),
+        ("draft", PlpTokenLimits),
+        ("tokens_out", _vp),
+        ("accepted_out", _vp),
+        ("logp_out", _vp),
+        ("kept_logp_out", _vp),
+    ]
+
+
 class PlpGradTensor(ctypes.Structure):
     _fields_ = [
         ("grad", _vp),
@@ -162,7 +200,8 @@ class PlpError(RuntimeError):
 _LATER = ("plp_layer_norm_fwd", "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd",
           "plp_adamw_step", "plp_sample_tokens_workspace_size", "plp_sample_tokens",
           "plp_embedding_fwd", "plp_embedding_bwd_workspace_size", "plp_embedding_bwd",
-          "plp_grad_norm_workspace_size", "plp_grad_norm", "plp_clip_grads")
+          "plp_grad_norm_workspace_size", "plp_grad_norm", "plp_clip_grads",
+          "plp_verify_tokens_workspace_size", "plp_verify_tokens")
 
 _lib = None
 
@@ -213,6 +252,8 @@ def lib() -> ctypes.CDLL:
     L.plp_grad_norm_workspace_size.argtypes = [P(PlpGradTensor), i32, P(sz)]
     L.plp_grad_norm.argtypes = [P(PlpGradTensor), i32, f64, f64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
     L.plp_clip_grads.argtypes = [P(PlpGradTensor), i32, _vp, _vp]
+    L.plp_verify_tokens_workspace_size.argtypes = [i64, i32, i32, i32, P(sz)]
+    L.plp_verify_tokens.argtypes = [P(PlpVerifyArgs), _vp, sz, _vp]
     L.plp_profile_start.argtypes = [ctypes.c_int32]
     L.plp_profile_stop.argtypes = [P(ctypes.c_double), P(ctypes.c_int32)]
     L.plp_profile_stop_n.argtypes = [P(ctypes.c_double), P(ctypes.c_int32), ctypes.c_int32]
@@ -226,7 +267,8 @@ def lib() -> ctypes.CDLL:
                  "plp_policy_loss_workspace_size", "plp_policy_loss_from_logprobs", "plp_layer_norm_fwd",
                  "plp_layer_norm_bwd_workspace_size", "plp_layer_norm_bwd", "plp_adamw_step", "plp_sample_tokens_workspace_size",
                  "plp_sample_tokens", "plp_embedding_fwd", "plp_embedding_bwd_workspace_size", "plp_embedding_bwd",
-                 "plp_grad_norm_workspace_size", "plp_grad_norm", "plp_clip_grads"):
+                 "plp_grad_norm_workspace_size", "plp_grad_norm", "plp_clip_grads",
+                 "plp_verify_tokens_workspace_size", "plp_verify_tokens"):
         getattr(L, name).restype = ctypes.c_int
     if L.plp_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI version {L.plp_abi_version()}, this binding {ABI_VERSION}: "
