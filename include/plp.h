@@ -518,8 +518,7 @@ PLP_API int plp_embedding_fwd(const int64_t* tokens, const void* weight, int64_t
  * grad_weight_dtype: grad_y's, or fp32. N = 0 gives zeros, or with `accumulate`
  * does nothing. Errors as above, and PLP_E_WORKSPACE; PLP_E_UNSUPPORTED for a
  * bf16 grad_weight of an fp32 grad_y. */
-PLP_API int plp_embedding_bwd_workspace_size(int64_t N, int32_t H, int32_t V, int32_t grad_y_dtype, int32_t accumulate,
-                                             size_t* bytes);
+PLP_API int plp_embedding_bwd_workspace_size(int64_t N, int32_t H, int32_t V, int32_t grad_y_dtype, size_t* bytes);
 PLP_API int plp_embedding_bwd(const int64_t* tokens, const void* grad_y, int64_t N, int32_t H, int32_t V,
                               int32_t grad_y_dtype, int32_t grad_weight_dtype, float scale, int32_t accumulate,
                               void* grad_weight, void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -247,7 +247,7 @@ def lib() -> ctypes.CDLL:
     L.plp_sample_tokens_workspace_size.argtypes = [i64, i32, P(sz)]
     L.plp_sample_tokens.argtypes = [P(PlpSampleArgs), _vp, sz, _vp]
     L.plp_embedding_fwd.argtypes = [_vp, _vp, i64, i32, i32, i32, ctypes.c_float, _vp, _vp]
-    L.plp_embedding_bwd_workspace_size.argtypes = [i64, i32, i32, i32, i32, P(sz)]
+    L.plp_embedding_bwd_workspace_size.argtypes = [i64, i32, i32, i32, P(sz)]
     L.plp_embedding_bwd.argtypes = [_vp, _vp, i64, i32, i32, i32, i32, ctypes.c_float, i32, _vp, _vp, sz, _vp]
     L.plp_grad_norm_workspace_size.argtypes = [P(PlpGradTensor), i32, P(sz)]
     L.plp_grad_norm.argtypes = [P(PlpGradTensor), i32, f64, f64, _vp, _vp, _vp, _vp, _vp, sz, _vp]

@@ -19,7 +19,6 @@ namespace plp {
 namespace {
 
 constexpr int NT = 256;
-constexpr int FT = 1024;  // threads that finish
 
 template <typename T>
 constexpr int vec_of = 16 / (int)sizeof(T);
@@ -107,31 +106,29 @@ __global__ __launch_bounds__(NT) void grad_squares_kernel(const GradLaunch a, do
   }
 }
 
-// Workgroup 0 the whole norm, the others the tensors' norms, a wave each.
-__global__ __launch_bounds__(FT) void grad_finish_kernel(const GradFinish a) {
+// Workgroup 0 the whole norm, the others a tensor's each.
+__global__ __launch_bounds__(NT) void grad_finish_kernel(const GradFinish a) {
+  __shared__ double red[NT / 64];
   const double given = a.grad_scale ? (double)*a.grad_scale : 1.0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t i = blockIdx.x - 1;  // not of workgroup 0
+  uint32_t from = 0, to = a.tiles;
   if (blockIdx.x > 0) {
-    const uint32_t i = (blockIdx.x - 1) * (FT / 64) + wave;
-    if (i >= a.count) return;
-    const uint32_t end = i + 1 < a.count ? a.start[i + 1] : a.tiles;
-    double s = 0.0;
-    for (uint32_t k = a.start[i] + lane; k < end; k += 64) s += a.part[k];
-    s = wave_sum(s);
-    if (lane == 0) a.norms[i] = (float)(fabs(given) * sqrt(s));
-    return;
+    from = a.start[i];
+    if (i + 1 < a.count) to = a.start[i + 1];
   }
-  __shared__ double red[FT / 64];
   double s = 0.0;
-  for (uint32_t k = threadIdx.x; k < a.tiles; k += FT) s += a.part[k];
+#pragma unroll 8
+  for (uint32_t k = from + threadIdx.x; k < to; k += NT) s += a.part[k];
   s = wave_sum(s);
-  if (lane == 0) red[wave] = s;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.0;
-    for (int w = 0; w < FT / 64; ++w) s += red[w];
-    const double norm = fabs(given) * sqrt(s);
-    const float n32 = (float)norm;
+  if (threadIdx.x > 0) return;
+  s = (red[0] + red[1]) + (red[2] + red[3]);
+  const double norm = fabs(given) * sqrt(s);
+  const float n32 = (float)norm;
+  if (blockIdx.x > 0) {
+    a.norms[i] = n32;
+  } else {
     a.norm[0] = n32;
     a.scale[0] = fabsf(n32) < INFINITY ? (float)(given * fmin(1.0, a.max_norm / (norm + a.eps))) : NAN;
   }
@@ -177,8 +174,7 @@ hipError_t launch_grad_squares(const GradLaunch& a, double* part, uint32_t* star
 }
 
 hipError_t launch_grad_finish(const GradFinish& a, hipStream_t st) {
-  const uint32_t others = a.norms ? (a.count + FT / 64 - 1) / (FT / 64) : 0;
-  grad_finish_kernel<<<1 + others, FT, 0, st>>>(a);
+  grad_finish_kernel<<<1 + (a.norms ? a.count : 0), NT, 0, st>>>(a);
   return hipGetLastError();
 }
 

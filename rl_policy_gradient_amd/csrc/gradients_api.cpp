@@ -26,16 +26,17 @@ int check_embed_sizes(int64_t N, int32_t H, int32_t V, int32_t dtype) {
 size_t carve_embed_bwd(void* ws, EmbedBwd& a) {
   Carver c(ws);
   if (a.N == 0) return 0;
-  const EmbedBwdPlan p = embed_bwd_plan(a.N, a.H, a.V, a.grad_y_dtype, a.accumulate);
+  const EmbedBwdPlan p = embed_bwd_plan(a.N, a.H, a.V, a.grad_y_dtype);
   const size_t n = (size_t)a.N;
   a.key[0] = c.take<uint32_t>(n);
   a.pos[0] = c.take<uint32_t>(n);
   const bool more = p.radix && p.passes > 1;
   a.key[1] = c.take<uint32_t>(more ? n : 0);
   a.pos[1] = c.take<uint32_t>(more ? n : 0);
-  for (uint32_t*& h : a.hist) h = c.take<uint32_t>(p.radix ? (size_t)p.blocks << p.bits : 0);
-  a.head_row = c.take<int32_t>((size_t)p.ranges);
+  a.hist = c.take<uint32_t>(p.radix ? (size_t)p.blocks << p.bits : 0);
   a.tail_row = c.take<int32_t>((size_t)p.ranges);
+  a.shared_rows = c.take<uint32_t>(1);
+  a.shared_list = c.take<uint2>((size_t)p.ranges);
   a.head = c.take<float>((size_t)p.ranges * a.H);
   a.tail = c.take<float>((size_t)p.ranges * a.H);
   return c.off;
@@ -45,9 +46,9 @@ size_t carve_embed_bwd(void* ws, EmbedBwd& a) {
 constexpr int64_t kMaxGradNumel = (int64_t)1 << 40;
 constexpr int kMaxGrads = 1 << 20;
 // Elements of a tile, log2: at least 2048 (a load of 16 bytes a thread for
-// bf16), and at most some 8192 tiles for the finishing workgroup to add.
+// bf16), and at most some 4096 tiles for the finishing workgroup to add.
 constexpr int kMinTileShift = 11;
-constexpr int64_t kMostTiles = 8192;
+constexpr int64_t kMostTiles = 4096;
 
 int check_grads(const plp_grad_tensor* t, int32_t count, int64_t* total) {
   if (count < 0 || count > kMaxGrads || (count > 0 && !t))
@@ -132,8 +133,7 @@ PLP_API int plp_embedding_fwd(const int64_t* tokens, const void* weight, int64_t
   return ok();
 }
 
-PLP_API int plp_embedding_bwd_workspace_size(int64_t N, int32_t H, int32_t V, int32_t grad_y_dtype, int32_t accumulate,
-                                             size_t* bytes) {
+PLP_API int plp_embedding_bwd_workspace_size(int64_t N, int32_t H, int32_t V, int32_t grad_y_dtype, size_t* bytes) {
   if (!bytes) return fail(PLP_E_INVALID, "bytes is NULL");
   int rc = check_embed_sizes(N, H, V, grad_y_dtype);
   if (rc) return rc;
@@ -142,7 +142,6 @@ PLP_API int plp_embedding_bwd_workspace_size(int64_t N, int32_t H, int32_t V, in
   a.H = H;
   a.V = V;
   a.grad_y_dtype = grad_y_dtype;
-  a.accumulate = accumulate ? 1 : 0;
   *bytes = carve_embed_bwd(nullptr, a);
   return ok();
 }

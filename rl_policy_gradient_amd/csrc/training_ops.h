@@ -61,10 +61,11 @@ struct EmbedBwdPlan {
   int blocks;        // workgroups of a radix pass
   int64_t per;       // tokens of each
   int slices;        // column slices of a row
-  int items;         // rows and tokens of one range
+  int items;         // tokens of one range
   int64_t ranges;
+  bool shared;       // whether ranges can share a row
 };
-EmbedBwdPlan embed_bwd_plan(int64_t N, int H, int V, int grad_y_dtype, bool accumulate);
+EmbedBwdPlan embed_bwd_plan(int64_t N, int H, int V, int grad_y_dtype);
 struct EmbedBwd {
   const int64_t* tokens;
   const void* grad_y;
@@ -74,9 +75,12 @@ struct EmbedBwd {
   float scale;
   // workspace
   uint32_t *key[2], *pos[2];    // [N] each; the second pair with radix passes only
-  uint32_t* hist[3];            // [blocks][1 << bits] each, with radix passes only
-  float *head, *tail;           // [ranges][H] partial sums of rows that ranges share
-  int32_t *head_row, *tail_row; // [ranges] the rows they are of, or -1
+  uint32_t* hist;               // [blocks][1 << bits], with radix passes only
+  float *head, *tail;           // [ranges][H] partial sums of rows that ranges share: of the range they
+                                // end in, and of those before
+  int32_t* tail_row;            // [ranges] the row that tail is of, or -1
+  uint32_t* shared_rows;        // how many ranges have a head
+  uint2* shared_list;           // [ranges] which, and the rows they are of
 };
 hipError_t launch_embed_bwd(const EmbedBwd& a, hipStream_t st);
 

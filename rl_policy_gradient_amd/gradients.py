@@ -69,7 +69,7 @@ def embedding_bwd(grad_y: torch.Tensor, tokens: torch.Tensor, V: int, *, scale: 
     L = _abi.lib()
     n = ctypes.c_size_t()
     gdt, acc = _dtype_code(grad_y), 1 if accumulate else 0
-    _abi.check(L.plp_embedding_bwd_workspace_size(N, H, V, gdt, acc, ctypes.byref(n)))
+    _abi.check(L.plp_embedding_bwd_workspace_size(N, H, V, gdt, ctypes.byref(n)))
     with _on(dev):
         gw = _out(out, "grad_weight", (V, H), dtype, dev)
         ws = _workspace(n.value, dev, workspace)

@@ -46,9 +46,9 @@ def test_embedding_forward_refuses(kw, code, msg):
     assert msg in _err()
 
 
-def need(N=8, H=64, V=100, dt=abi.DTYPE_BF16, acc=0):
+def need(N=8, H=64, V=100, dt=abi.DTYPE_BF16):
     n = ctypes.c_size_t()
-    return _lib().plp_embedding_bwd_workspace_size(N, H, V, dt, acc, ctypes.byref(n)), n.value
+    return _lib().plp_embedding_bwd_workspace_size(N, H, V, dt, ctypes.byref(n)), n.value
 
 
 def bwd(**kw):
@@ -84,14 +84,13 @@ def test_embedding_of_nothing_and_workspace():
         for H in (1, 896, 65536):
             for V in (1, 1000, 151936, (1 << 31) - 1):
                 for dt in (abi.DTYPE_BF16, abi.DTYPE_F32):
-                    for acc in (0, 1):
-                        rc, n = need(N, H, V, dt, acc)
-                        assert rc == abi.PLP_OK and n % 256 == 0
-                        # two pairs of 32-bit words a token, three tables of 256 x 1024, and partial sums of
-                        # 16384 waves' columns on either side (512 or 256 of them), 4 bytes each
-                        assert 8 * N <= n <= 16 * N + 3 * (1 << 20) + 2 * 4 * (16384 + 256) * 512 + 2 * 4 * 16385 + 4096
+                    rc, n = need(N, H, V, dt)
+                    assert rc == abi.PLP_OK and n % 256 == 0
+                    # two pairs of 32-bit words a token, a table of 256 x 1024, partial sums of some 8192 waves'
+                    # columns on either side (512 or 256 of them) and 12 bytes a range
+                    assert 8 * N <= n <= 16 * N + (1 << 20) + 2 * 4 * (8192 + 256) * 512 + 12 * 8448 + 4096
     assert need(H=0)[0] == abi.PLP_E_INVALID and need(dt=3)[0] == abi.PLP_E_INVALID
-    assert _lib().plp_embedding_bwd_workspace_size(1, 1, 1, 0, 0, None) == abi.PLP_E_INVALID
+    assert _lib().plp_embedding_bwd_workspace_size(1, 1, 1, 0, None) == abi.PLP_E_INVALID
 
 
 def grads(n=3, **kw):
