@@ -60,9 +60,11 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
   const int lane = threadIdx.x % kStatLanes;
   const int b = blockIdx.x * kStatBlocks + threadIdx.x / kStatLanes;
   if (b >= r.blocks()) return;  // the same for the 16 lanes
+  typename Row<T>::Raw raw[kStatChunks];
+  fetch_block(r, b, lane, raw);
   float m;
   double s;
-  block_stats(r, b, lane, temperature_of(a, row), m, s);
+  block_stats<T>(raw, temperature_of(a, row), m, s);
   if (lane == 0) {
     a.block_max[row * G + b] = m;
     a.block_sum[row * G + b] = s;

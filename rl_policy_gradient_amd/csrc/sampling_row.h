@@ -195,11 +195,16 @@ struct MaxOrNan {
 
 // Block b of a row, by its 16 lanes (`lane` of them).
 template <typename T>
-__device__ __forceinline__ void block_stats(const Row<T>& r, int b, int lane, float tau, float& m, double& s) {
+__device__ __forceinline__ void fetch_block(const Row<T>& r, int b, int lane, typename Row<T>::Raw (&raw)[kStatChunks]) {
+#pragma unroll
+  for (int c = 0; c < kStatChunks; ++c) raw[c] = r.fetch(b * kLanes + c * kStatLanes + lane);
+}
+template <typename T>
+__device__ __forceinline__ void block_stats(const typename Row<T>::Raw (&raw)[kStatChunks], float tau, float& m, double& s) {
   const double rate = rate_of(tau), least = least_of(tau);
   float z[kStatChunks][kChunk];
 #pragma unroll
-  for (int c = 0; c < kStatChunks; ++c) r.load(b * kLanes + c * kStatLanes + lane, z[c]);
+  for (int c = 0; c < kStatChunks; ++c) Row<T>::values(raw[c], z[c]);
   m = z[0][0];
 #pragma unroll
   for (int c = 0; c < kStatChunks; ++c)

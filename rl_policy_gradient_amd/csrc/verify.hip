@@ -16,10 +16,11 @@
 // and which token is drawn can so change only where a border lies within about
 // 1e-13 of a uniform number.
 //
-// Four launches: the statistics of every row's blocks and the rows' cuts and
-// masses, as in sampling; then the acceptance, which each workgroup decides for
-// itself, and the blocks' sums of what is left of the sequence's last row; then
-// one workgroup a sequence for the token.
+// Four launches: the statistics of every row's blocks, as in sampling; the
+// rows' cuts and masses, and from them the chances of the drafted token; the
+// acceptance, which each workgroup decides for itself, and the blocks' sums of
+// what is left of the sequence's last row; and one workgroup a sequence for the
+// token.
 #include "sampling_row.h"
 #include "verify_ops.h"
 
@@ -56,20 +57,99 @@ __global__ __launch_bounds__(kStatThreads) void verify_stats_kernel(VerifyArgs a
   const int64_t row = blockIdx.y;
   const Place at = place_of_row(a, row, per);
   if (!used(a, at)) return;
+  if (blockIdx.x == 0 && at.j == 0 && !at.draft) {  // what the next launch says of the sequence's drafts
+    if (threadIdx.x == 0) a.refused[at.seq] = a.K;
+    for (int k = threadIdx.x; k < 2 * a.K; k += kStatThreads) a.chance[at.seq * a.K * 2 + k] = -1.0;
+  }
   const VerifyRows& src = a.of[at.draft];
   const Row<T> r(logits_of<T>(src, at.seq, at.j), a.V);
-  const int b = blockIdx.x * kStatBlocks + threadIdx.x / kStatLanes;
+  const int b = blockIdx.x * kStatBlocks + threadIdx.x / kStatLanes, lane = threadIdx.x % kStatLanes;
   if (b >= r.blocks()) return;  // the same for the 16 lanes
+  typename Row<T>::Raw raw[kStatChunks];
+  fetch_block(r, b, lane, raw);
   float m;
   double s;
-  block_stats(r, b, threadIdx.x % kStatLanes, src.tau_seq ? src.tau_seq[at.seq] : src.tau, m, s);
-  if (threadIdx.x % kStatLanes == 0) {
+  block_stats<T>(raw, src.tau_seq ? src.tau_seq[at.seq] : src.tau, m, s);
+  if (lane == 0) {
     a.block_max[row * G + b] = m;
     a.block_sum[row * G + b] = s;
   }
 }
 
-// What sampling's row kernel finds before it draws.
+// The probabilities of a row's tokens. Nothing is contracted, so that a token's
+// is the same wherever it is formed.
+struct Chance {
+  double m, rate, inv, least;
+  float cut, lowest;  // lowest: what weighs 2^-1000 of the largest
+  int upto, state;
+  __device__ explicit Chance(const VerifyRow& r)
+      : m((double)r.most),
+        rate(rate_of(r.tau)),
+        inv(1.0 / r.mass),
+        least((double)r.least),
+        cut(r.cut),
+        lowest(lowest_of(r)),
+        upto(r.upto),
+        state(r.state) {}
+  // The least value whose distance to the largest exp2_of takes.
+  __device__ static __forceinline__ float lowest_of(const VerifyRow& r) {
+    const double z = (double)r.most + least_of(r.tau);
+    const float f = (float)z;
+    return (double)f < z ? Key<float>::value(Key<float>::of(f) + 1) : f;
+  }
+  __device__ __forceinline__ bool kept(float z, int e) const {
+    return state == kOneToken ? e == upto : z > cut || (z == cut && e <= upto);
+  }
+  // Of token e with logit z. (What weighs 2^-1000 of the largest, or less, is nothing.)
+  __device__ __forceinline__ double of(float z, int e) const {
+#pragma clang fp contract(off)
+    if (state == kOneToken) return e == upto ? 1.0 : 0.0;  // uniform
+    const double w = exp2_of((double)fmaxf(z, lowest) - m, rate);
+    return (kept(z, e) & (z >= lowest) & (w >= least)) ? w * inv : 0.0;
+  }
+};
+
+// A number that another workgroup of the launch may look at while this one runs.
+__device__ __forceinline__ void publish(double* p, double v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V_>
+__device__ __forceinline__ V_ seen(const V_* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Whether a draft is accepted, of a uniform and the chances of it. (False for NaN.)
+__device__ __forceinline__ bool accepts(float u, double own, double chance) {
+  return u == u && (double)fminf(fmaxf(u, 0.f), 0x1.fffffep-1f) * own < chance;
+}
+
+// One thread: the row as it was found, and the chance of its drafted token d
+// (-1: there is none), whose logit is z.
+__device__ __forceinline__ void leave_row(const VerifyArgs& a, int64_t row, const Place& at, const VerifyRow& r, int d,
+                                          float z) {
+  a.rows[row] = r;
+  if (at.j >= a.K) return;
+  const double mine = r.state == kNoRow ? (double)NAN : d < 0 ? 0.0 : Chance(r).of(z, d);
+  double* const both = a.chance + (at.seq * a.K + at.j) * 2;
+  if (!a.skip) {
+    both[at.draft] = mine;
+    return;
+  }
+  publish(both + at.draft, mine);
+  // the rows after a draft that is refused need not be looked at: an earlier
+  // end of the launch, and nothing else, depends on who sees what when
+  const double other = a.of[1].logits ? seen(both + (1 - at.draft)) : 1.0;
+  if (other < 0.0) return;  // not known yet, or not to this workgroup
+  if (!accepts(a.uniforms[at.seq * (a.K + 1) + at.j], at.draft ? mine : other, at.draft ? other : mine))
+    __hip_atomic_fetch_min(a.refused + at.seq, at.j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What sampling's row kernel finds before it draws. With `skip` rows go by their
+// place in the sequence, the first of all sequences first (a target's row, then
+// the draft's): a launch of many more rows than run at once (one a CU, with
+// limits) then meets many whose sequence has a draft refused before them, and
+// leaves them out (256 x 8 certain drafts at 32000, top_p 0.95: 84 us, 143 with
+// every row). Otherwise a sequence's rows follow each other (384 rows of 96 x 3
+// drafts: 47 us, 62 by their place).
 template <typename T, bool LIMITS>
 __global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, int G) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -78,12 +158,25 @@ __global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, i
   float* bmax = reinterpret_cast<float*>(bq + G);
   uint16_t* act = reinterpret_cast<uint16_t*>(bmax + G);
   Lists& ls = *reinterpret_cast<Lists*>(lds + shared_bytes(G));
-  const int64_t row = blockIdx.x;
-  const Place at = place_of_row(a, row, per);
+  Place at = place_of_row(a, blockIdx.x, per);
+  if (a.skip) {
+    const int slot = (int)(blockIdx.x / (uint32_t)a.B);
+    at.seq = blockIdx.x - slot * (uint32_t)a.B;
+    at.j = a.of[1].logits ? slot / 2 : slot;
+    at.draft = a.of[1].logits ? slot % 2 : 0;
+  }
   if (!used(a, at)) return;
+  const int64_t row = at.seq * per + (at.draft ? a.K + 1 : 0) + at.j;
   const VerifyRows& src = a.of[at.draft];
   const Row<T> r(logits_of<T>(src, at.seq, at.j), a.V);
   const int nb = r.blocks();
+  int refused = a.K, drafted = -1;  // drafted: the token whose chance is asked for
+  float logit = 0.f;
+  if (threadIdx.x == 0 && a.skip && at.j > 0) refused = seen(a.refused + at.seq);
+  if (threadIdx.x == 0 && at.j < a.K) {
+    const int64_t d = a.draft_tokens[at.seq * a.K + at.j];
+    drafted = d >= 0 && d < a.V ? (int)d : -1;
+  }
   const float tau = src.tau_seq ? src.tau_seq[at.seq] : src.tau;
   const float top_p = src.top_p_seq ? src.top_p_seq[at.seq] : src.top_p;
   const float min_p = src.min_p_seq ? src.min_p_seq[at.seq] : src.min_p;
@@ -91,14 +184,18 @@ __global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, i
 
   float mf, lowest_max;
   int nan;
+  if (a.skip && threadIdx.x == 0) sh.place = (u64)refused;
   load_blocks(sh, bmax, bq, a.block_max + row * G, a.block_sum + row * G, nb, mf, lowest_max, nan);
+  if (a.skip && uniform(sh.place) < (u64)at.j) return;
+  if (drafted >= 0) logit = (float)r.p[drafted];
   if (!has_distribution(mf, nan, tau, top_p, min_p)) {
-    if (threadIdx.x == 0) a.rows[row].state = kNoRow;
+    if (threadIdx.x == 0) leave_row(a, row, at, VerifyRow{1.0, 1.0, 0.f, 1.f, -1.f, 0.f, -1, kNoRow}, drafted, logit);
     return;
   }
   if (tau == 0.f) {
     find_first(sh, r, bmax, mf, nb);
-    if (threadIdx.x == 0) a.rows[row] = VerifyRow{1.0, 1.0, mf, tau, -1.f, 0.f, sh.bin, kOneToken};
+    if (threadIdx.x == 0)
+      leave_row(a, row, at, VerifyRow{1.0, 1.0, mf, tau, -1.f, 0.f, sh.bin, kOneToken}, drafted, logit);
     return;
   }
   RowSampler<T> s{r, sh, ls, bmax, bq, act, nb, mf, uniform((double)mf), uniform(rate_of(tau)),
@@ -107,83 +204,64 @@ __global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, i
   const int each = (nb + NT - 1) / NT;
   const int b0 = min(nb, (int)threadIdx.x * each), b1 = min(nb, b0 + each);
   weigh_blocks(s, b0, b1);
+  VerifyRow out{s.S, s.S, mf, tau, -1.f, -INFINITY, -1, kWeights};
   if (LIMITS && ((top_k > 0 && top_k < a.V) || top_p < 1.f || min_p > 0.f)) {
     const u64 cut = s.cut(top_k, top_p, lowest_max);
     u64 mine = 0, total;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) mine += bq[b];
     block_scan(mine, sh.scan64, total);
-    if (threadIdx.x == 0)
-      a.rows[row] = VerifyRow{(double)total / s.unit, s.S, mf, tau, (float)s.least, s.value_at(cut), index_at(cut), kWeights};
-  } else if (threadIdx.x == 0) {
-    a.rows[row] = VerifyRow{s.S, s.S, mf, tau, -1.f, -INFINITY, -1, kWeights};
+    out = VerifyRow{(double)total / s.unit, s.S, mf, tau, (float)s.least, s.value_at(cut), index_at(cut), kWeights};
   }
+  if (threadIdx.x == 0) leave_row(a, row, at, out, drafted, logit);
 }
 
-// The probability of a row's token e with logit z. The same bits wherever it is
-// formed: nothing is contracted.
-struct Chance {
-  double m, rate, least_d, inv, least;
-  float cut;
-  int upto, state;
-  __device__ explicit Chance(const VerifyRow& r)
-      : m((double)r.most),
-        rate(rate_of(r.tau)),
-        least_d(least_of(r.tau)),
-        inv(1.0 / r.mass),
-        least((double)r.least),
-        cut(r.cut),
-        upto(r.upto),
-        state(r.state) {}
-  __device__ __forceinline__ bool kept(float z, int e) const {
-    return state == kOneToken ? e == upto : z > cut || (z == cut && e <= upto);
-  }
-  __device__ __forceinline__ double of(float z, int e) const {
-#pragma clang fp contract(off)
-    if (!kept(z, e)) return 0.0;
-    if (state == kOneToken) return 1.0;
-    const double d = (double)z - m;
-    const double w = exp2_of(fmax(d, least_d), rate);
-    return w >= least && d >= least_d ? w * inv : 0.0;  // 2^-1000 of the largest, or less, is nothing
-  }
-};
+// Lane l's value of a row.
+__device__ __forceinline__ VerifyRow row_of_lane(const VerifyRow& r, int l) {
+  return VerifyRow{lane_of(r.mass, l), lane_of(r.whole, l), lane_of(r.most, l), lane_of(r.tau, l),
+                   lane_of(r.least, l), lane_of(r.cut, l), lane_of(r.upto, l), lane_of(r.state, l)};
+}
 
-// Every thread of the workgroup gets the same verdict (`sh`: an int in LDS).
-template <typename T>
-__device__ __forceinline__ Verdict judge(const VerifyArgs& a, int64_t seq, int per, int* sh) {
-  const int n = drafts_of(a, seq);
-  const VerifyRow* rows = a.rows + seq * per;
+// The same verdict in every wave: lane l looks at draft l, and everything that
+// may be needed is loaded at once. More drafts than lanes go on in steps.
+__device__ __forceinline__ Verdict judge(const VerifyArgs& a, int64_t seq, int per) {
+  const int lane = threadIdx.x & 63, n = drafts_of(a, seq);
   const float* u = a.uniforms + seq * (a.K + 1);
-  if (threadIdx.x == 0) *sh = n;
-  __syncthreads();
-  for (int k = threadIdx.x; k < n; k += blockDim.x) {
-    const int64_t d = a.draft_tokens[seq * a.K + k];
-    const bool real = d >= 0 && d < a.V;
-    const VerifyRow p = rows[k];
-    bool yes = real && p.state != kNoRow && u[k] == u[k];
-    if (yes) {
-      const double chance = Chance(p).of((float)logits_of<T>(a.of[0], seq, k)[d], (int)d);
-      double own = 1.0;
-      if (a.of[1].logits) {
-        const VerifyRow q = rows[a.K + 1 + k];
-        yes = q.state != kNoRow;
-        if (yes) own = Chance(q).of((float)logits_of<T>(a.of[1], seq, k)[d], (int)d);
-      }
-      yes = yes && (double)fminf(fmaxf(u[k], 0.f), 0x1.fffffep-1f) * own < chance;
-    }
-    if (!yes) atomicMin(sh, k);
-  }
-  __syncthreads();
+  const bool logits = a.of[1].logits != nullptr;
+  const float last = u[a.K];
   Verdict v;
-  v.count = uniform(*sh);
-  v.refused = v.count < n ? 1 : 0;
-  v.state = rows[v.count].state;
-  if (u[a.K] != u[a.K]) v.state = kNoRow;
-  if (v.refused) {
-    if (u[v.count] != u[v.count]) v.state = kNoRow;
-    if (a.of[1].logits && rows[a.K + 1 + v.count].state == kNoRow) v.state = kNoRow;
+  for (int k0 = 0;; k0 += 64) {
+    const int k = min(k0 + lane, a.K), kd = min(k, a.K - 1);  // kd: -1 without drafts
+    const VerifyRow p = a.rows[seq * per + k];
+    VerifyRow q = p;
+    double own = 1.0, chance = 0.0;
+    int64_t d = -1;
+    if (kd >= 0) {
+      const double* both = a.chance + (seq * a.K + kd) * 2;
+      chance = both[0];
+      if (logits) {
+        own = both[1];
+        q = a.rows[seq * per + a.K + 1 + kd];
+      } else {
+        d = a.draft_tokens[seq * a.K + kd];
+      }
+    }
+    const float mine = u[k];
+    // the first that is refused, or is no draft. Past it rows and chances may
+    // not be known, and do not matter.
+    const u64 ends = __ballot(k0 + lane >= n || !accepts(mine, own, chance));
+    if (!ends) continue;
+    const int l = __builtin_ctzll(ends);
+    v.count = k0 + l;
+    v.refused = v.count < n ? 1 : 0;
+    v.p = row_of_lane(p, l);
+    v.q = row_of_lane(q, l);
+    const int64_t drafted = (int64_t)lane_of((u64)d, l);
+    v.certain = v.refused && !logits && drafted >= 0 && drafted < a.V ? (int)drafted : -1;
+    const float at = lane_of(mine, l);
+    v.state = last != last || (v.refused && (at != at || (logits && v.q.state == kNoRow))) ? kNoRow : v.p.state;
+    return v;
   }
-  return v;
 }
 
 // What the last token is drawn from: max(0, p - q), or p.
@@ -192,22 +270,16 @@ struct Rest {
   const T *zp, *zq;  // zq NULL: q is 1 at `certain`, or nothing (-1)
   Chance p, q;
   int certain;
-  __device__ Rest(const VerifyArgs& a, int64_t seq, int per, const Verdict& v)
+  __device__ Rest(const VerifyArgs& a, int64_t seq, const Verdict& v)
       : zp(logits_of<T>(a.of[0], seq, v.count)),
         zq(v.refused && a.of[1].logits ? logits_of<T>(a.of[1], seq, v.count) : nullptr),
-        p(a.rows[seq * per + v.count]),
-        q(a.rows[seq * per + (zq ? a.K + 1 + v.count : v.count)]),
-        certain(-1) {
-    if (v.refused && !a.of[1].logits) {
-      const int64_t d = a.draft_tokens[seq * a.K + v.count];
-      certain = d >= 0 && d < a.V ? (int)d : -1;
-    }
-  }
+        p(v.p),
+        q(v.q),
+        certain(v.certain) {}
   __device__ __forceinline__ double of(float z, float y, int e) const {
 #pragma clang fp contract(off)
     const double chance = p.of(z, e);
-    if (chance == 0.0) return 0.0;
-    if (zq) return fmax(chance - q.of(y, e), 0.0);
+    if (zq) return fmax(chance - q.of(y, e), 0.0);  // uniform
     return e == certain ? 0.0 : chance;
   }
 };
@@ -215,44 +287,52 @@ struct Rest {
 constexpr int kRestThreads = 256;
 constexpr int kRestBlocks = kRestThreads / 16;  // blocks at a time, 16 lanes each
 
+// The logits of a block of both rows that one of its 16 lanes takes, as they lie
+// in memory: nothing waits for the loads before they are used.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int e0, int V, float (&z)[kChunk]) {
+struct RestBlock {
   typedef T TV __attribute__((ext_vector_type(kChunk), aligned(sizeof(T))));
-  if (e0 + kChunk <= V) {
-    const TV t = *reinterpret_cast<const TV*>(p + e0);
+  TV z[2], y[2];
+  __device__ static __forceinline__ int first(int b, int lane, int c) { return b * kSampleBlock + (c * 16 + lane) * kChunk; }
+  __device__ static __forceinline__ TV load8(const T* p, int e0, int V) {
+    if (e0 + kChunk <= V) return *reinterpret_cast<const TV*>(p + e0);
+    TV t;
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) z[k] = (float)t[k];
-  } else {
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) z[k] = e0 + k < V ? (float)p[e0 + k] : -INFINITY;
+    for (int k = 0; k < kChunk; ++k) t[k] = e0 + k < V ? p[e0 + k] : (T)-INFINITY;
+    return t;
   }
-}
-
-// The sum of a block's chances, in each of its 16 lanes.
-template <typename T>
-__device__ __forceinline__ double block_rest(const Rest<T>& rest, int b, int lane, int V) {
-  double s = 0.0;
+  __device__ __forceinline__ void load(const Rest<T>& rest, int b, int lane, int V) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int e0 = b * kSampleBlock + (c * 16 + lane) * kChunk;
-    float z[kChunk], y[kChunk];
-    load8(rest.zp, e0, V, z);
-    bool any = false;
+    for (int c = 0; c < 2; ++c) z[c] = load8(rest.zp, first(b, lane, c), V);
+    if (rest.zq)  // uniform
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) any |= rest.p.kept(z[k], e0 + k);
-    if (!any) continue;
-    if (rest.zq) load8(rest.zq, e0, V, y);
-#pragma unroll
-    for (int k = 0; k < kChunk; ++k) s += e0 + k < V ? rest.of(z[k], rest.zq ? y[k] : 0.f, e0 + k) : 0.0;
+      for (int c = 0; c < 2; ++c) y[c] = load8(rest.zq, first(b, lane, c), V);
   }
-  return row_reduce(s, Add());
-}
+  // The sum of the block's chances, in each of its 16 lanes.
+  __device__ __forceinline__ double sum(const Rest<T>& rest, int b, int lane) const {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int e0 = first(b, lane, c);
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) any |= rest.p.kept((float)z[c][k], e0 + k);
+      if (!__any(any)) continue;  // most of a row with limits
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) s += rest.of((float)z[c][k], (float)y[c][k], e0 + k);  // 0 past the row's end
+    }
+    return row_reduce(s, Add());
+  }
+};
 
 // The verdict, and the outputs but for the last token.
 template <typename T>
 __device__ __forceinline__ void say(const VerifyArgs& a, int64_t seq, int per, const Verdict& v) {
   if (threadIdx.x == 0) {
-    a.verdicts[seq] = v;
+    Verdict w = v;
+    w.log_whole = log(v.p.whole);
+    w.log_mass = log(v.p.mass);
+    a.verdicts[seq] = w;
     a.accepted[seq] = v.count;
   }
   // the accepted drafts, and nothing after the last token
@@ -278,16 +358,25 @@ __device__ __forceinline__ void say(const VerifyArgs& a, int64_t seq, int per, c
 
 template <typename T>
 __global__ __launch_bounds__(kRestThreads) void verify_rest_kernel(VerifyArgs a, int per, int blocks, int each) {
-  __shared__ int sh;
   const int64_t seq = blockIdx.y;
-  const Verdict v = judge<T>(a, seq, per, &sh);
-  if (blockIdx.x == 0) say<T>(a, seq, per, v);
+  const Verdict v = judge(a, seq, per);
+  if (blockIdx.x == gridDim.x - 1) return say<T>(a, seq, per, v);  // none of the blocks are its
   if (v.state == kNoRow) return;
-  const Rest<T> rest(a, seq, per, v);
+  const Rest<T> rest(a, seq, v);
   const int lane = threadIdx.x & 15, end = min(blocks, ((int)blockIdx.x + 1) * each);
-  for (int b = blockIdx.x * each + (int)(threadIdx.x >> 4); b < end; b += kRestBlocks) {
-    const double s = block_rest(rest, b, lane, a.V);
+  int b = blockIdx.x * each + (int)(threadIdx.x >> 4);
+  if (b >= end) return;  // the same for the 16 lanes
+  RestBlock<T> next;
+  next.load(rest, b, lane, a.V);
+#pragma unroll 1
+  for (;;) {
+    const RestBlock<T> now = next;
+    const int then = b + kRestBlocks;
+    if (then < end) next.load(rest, then, lane, a.V);
+    const double s = now.sum(rest, b, lane);
     if (lane == 0) a.rest[seq * blocks + b] = s;
+    if (then >= end) break;
+    b = then;
   }
 }
 
@@ -297,8 +386,17 @@ struct Pick {
   double before;
 };
 
+// The least `first` and the largest `last` of the threads, which both grow with
+// the thread, from one lane a wave.
+__device__ __forceinline__ void say_ends(Pick& sh, int first, int last) {
+  const u64 a = __ballot(first < 0x7fffffff), b = __ballot(last >= 0);
+  const int lane = threadIdx.x & 63;
+  if (a && lane == __builtin_ctzll(a)) atomicMin(&sh.first, first);
+  if (b && lane == 63 - __clzll((long long)b)) atomicMax(&sh.last, last);
+}
+
 template <typename T>
-__global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int per, int blocks) {
+__global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int blocks) {
   __shared__ Pick sh;
   const int64_t seq = blockIdx.x;
   const Verdict v = a.verdicts[seq];
@@ -315,7 +413,7 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int per, 
     }
     return;
   }
-  Rest<T> rest(a, seq, per, v);
+  Rest<T> rest(a, seq, v);
   double* sums = a.rest + seq * blocks;
   const int each = (blocks + NT - 1) / NT;
   const int b0 = min(blocks, (int)threadIdx.x * each), b1 = min(blocks, b0 + each);
@@ -329,7 +427,9 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int per, 
     rest.zq = nullptr;
     rest.certain = -1;
     for (int b = threadIdx.x >> 4; b < blocks; b += NT / 16) {
-      const double s = block_rest(rest, b, threadIdx.x & 15, a.V);
+      RestBlock<T> now;
+      now.load(rest, b, threadIdx.x & 15, a.V);
+      const double s = now.sum(rest, b, threadIdx.x & 15);
       if ((threadIdx.x & 15) == 0) sums[b] = s;
     }
     __threadfence_block();
@@ -349,8 +449,7 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int per, 
       if (run > target) first = min(first, b);
     }
   }
-  if (first < 0x7fffffff) atomicMin(&sh.first, first);
-  if (last >= 0) atomicMax(&sh.last, last);
+  say_ends(sh, first, last);
   __syncthreads();
   const int block = uniform(sh.first < 0x7fffffff ? sh.first : sh.last);
   if (block >= b0 && block < b1) {
@@ -370,24 +469,25 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int per, 
   }
   double all;
   const double upto = block_scan(r, sh.scan, all) + r;  // its barriers are after the resets
-  if (r > 0.0) {
-    atomicMax(&sh.last, e);
-    if (upto > inside) atomicMin(&sh.first, e);
-  }
+  say_ends(sh, r > 0.0 && upto > inside ? e : 0x7fffffff, r > 0.0 ? e : -1);
   __syncthreads();
   if (e == (sh.first < 0x7fffffff ? sh.first : sh.last) && threadIdx.x < kSampleBlock) {
-    const VerifyRow row = a.rows[seq * per + v.count];
+    const VerifyRow& row = v.p;
     float lp = 0.f, kp = 0.f;
     if (row.state == kWeights) {
       const double x = ((double)z - (double)row.most) / (double)row.tau;
-      lp = (float)(x - log(row.whole));
-      kp = (float)(x - log(row.mass));
+      lp = (float)(x - v.log_whole);
+      kp = (float)(x - v.log_mass);
     }
     a.tokens[at] = e;
     if (a.logp) a.logp[at] = lp;
     if (a.kept_logp) a.kept_logp[at] = kp;
   }
 }
+
+// Rows of a launch above which they look at what is refused before them: some
+// four a CU, of which one runs at once.
+constexpr unsigned kSkipRows = 1024;
 
 bool limited(const VerifyRows& r, int V) {
   return r.top_k_seq || r.top_p_seq || r.min_p_seq || (r.top_k > 0 && r.top_k < V) || r.top_p < 1.f || r.min_p > 0.f;
@@ -421,6 +521,7 @@ hipError_t verify(const VerifyArgs& all, hipStream_t st) {
     if (all.logp) a.logp = all.logp + s0 * (all.K + 1);
     if (all.kept_logp) a.kept_logp = all.kept_logp + s0 * (all.K + 1);
     const unsigned rows = (unsigned)(a.B * per);
+    a.skip = limits && rows > kSkipRows;
     verify_stats_kernel<T><<<dim3((G + kStatBlocks - 1) / kStatBlocks, rows), kStatThreads, 0, st>>>(a, per, G);
     if (hipError_t e = hipGetLastError()) return e;
     if (limits)
@@ -432,9 +533,9 @@ hipError_t verify(const VerifyArgs& all, hipStream_t st) {
     const int sets = (blocks + kRestBlocks - 1) / kRestBlocks;
     const int splits = (int)std::min<int64_t>(sets, std::max<int64_t>(1, 2048 / a.B));
     const int each = (sets + splits - 1) / splits * kRestBlocks;
-    verify_rest_kernel<T><<<dim3((blocks + each - 1) / each, (unsigned)a.B), kRestThreads, 0, st>>>(a, per, blocks, each);
+    verify_rest_kernel<T><<<dim3((blocks + each - 1) / each + 1, (unsigned)a.B), kRestThreads, 0, st>>>(a, per, blocks, each);
     if (hipError_t e = hipGetLastError()) return e;
-    verify_pick_kernel<T><<<(unsigned)a.B, NT, 0, st>>>(a, per, blocks);
+    verify_pick_kernel<T><<<(unsigned)a.B, NT, 0, st>>>(a, blocks);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;

@@ -24,6 +24,8 @@ size_t carve_verify(void* ws, int64_t B, int32_t K, int32_t V, bool drafts, Veri
   a.block_sum = c.take<double>(rows * sample_blocks(V));
   a.block_max = c.take<float>(rows * sample_blocks(V));
   a.rows = c.take<VerifyRow>(rows);
+  a.chance = c.take<double>((size_t)B * K * 2);
+  a.refused = c.take<int32_t>((size_t)B);
   a.verdicts = c.take<Verdict>((size_t)B);
   a.rest = c.take<double>((size_t)B * verify_blocks(V));
   return c.off;

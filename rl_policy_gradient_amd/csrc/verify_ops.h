@@ -29,11 +29,14 @@ struct VerifyRow {
 };
 enum { kNoRow = 0, kWeights = 1, kOneToken = 2 };
 
-// How far a sequence is accepted.
+// How far a sequence is accepted, and what its last token is drawn from.
 struct Verdict {
   int32_t count;    // drafts accepted
   int32_t refused;  // whether the next one was refused
-  int32_t state;    // of what the last token is drawn from: kNoRow if that is no distribution
+  int32_t state;    // kNoRow if the last token has no distribution
+  int32_t certain;  // the refused draft where drafts are certain, or -1
+  double log_whole, log_mass;  // of the target's row
+  VerifyRow p, q;   // the target's row; the draft's, if a draft was refused and has one
 };
 struct VerifyArgs {
   VerifyRows of[2];  // the targets', and the drafts', whose logits are NULL if they are certain
@@ -48,10 +51,13 @@ struct VerifyArgs {
   double* block_sum;
   float* block_max;
   VerifyRow* rows;
+  double* chance;       // [B][K][2] of each draft: the target's chance of it, and the draft's own
+  int32_t* refused;     // [B] a draft that is refused, as far as is known
   Verdict* verdicts;
   double* rest;
   int64_t B;
   int K, V, dtype;
+  int skip;  // whether rows look at `refused`
 };
 constexpr int kVerifyMaxK = 1024;
 inline int verify_rows(int K, bool drafts) { return K + 1 + (drafts ? K : 0); }
