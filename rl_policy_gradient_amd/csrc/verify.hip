@@ -80,15 +80,17 @@ __global__ __launch_bounds__(kStatThreads) void verify_stats_kernel(VerifyArgs a
 // is the same wherever it is formed.
 struct Chance {
   double m, rate, inv, least;
-  float cut, lowest;  // lowest: what weighs 2^-1000 of the largest
+  float lowest;      // what weighs 2^-1000 of the largest
+  float cut, above;  // kept is what is at or above them, up to index `upto` and past it
   int upto, state;
   __device__ explicit Chance(const VerifyRow& r)
       : m((double)r.most),
         rate(rate_of(r.tau)),
         inv(1.0 / r.mass),
         least((double)r.least),
-        cut(r.cut),
         lowest(lowest_of(r)),
+        cut(fmaxf(r.cut, lowest)),
+        above(fmaxf(Key<float>::value(Key<float>::of(r.cut) + 1), lowest)),
         upto(r.upto),
         state(r.state) {}
   // The least value whose distance to the largest exp2_of takes.
@@ -97,15 +99,39 @@ struct Chance {
     const float f = (float)z;
     return (double)f < z ? Key<float>::value(Key<float>::of(f) + 1) : f;
   }
-  __device__ __forceinline__ bool kept(float z, int e) const {
-    return state == kOneToken ? e == upto : z > cut || (z == cut && e <= upto);
-  }
-  // Of token e with logit z. (What weighs 2^-1000 of the largest, or less, is nothing.)
-  __device__ __forceinline__ double of(float z, int e) const {
+  // Of N tokens with logits z from e0 on. (What weighs 2^-1000 of the largest,
+  // or less, is nothing.) The decisions that are the same for all are made
+  // outside the loops, so that these have no branches.
+  template <int N>
+  __device__ __forceinline__ void of(const float (&z)[N], int e0, double (&chance)[N]) const {
 #pragma clang fp contract(off)
-    if (state == kOneToken) return e == upto ? 1.0 : 0.0;  // uniform
-    const double w = exp2_of((double)fmaxf(z, lowest) - m, rate);
-    return (kept(z, e) & (z >= lowest) & (w >= least)) ? w * inv : 0.0;
+    if (state == kOneToken) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) chance[k] = e0 + k == upto ? 1.0 : 0.0;
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) chance[k] = exp2_of((double)fmaxf(z[k], lowest) - m, rate);
+    if (least > 0.0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) chance[k] = chance[k] >= least ? chance[k] : 0.0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) chance[k] = z[k] >= (e0 + k <= upto ? cut : above) ? chance[k] * inv : 0.0;
+  }
+  __device__ __forceinline__ double of(float z, int e) const {
+    const float one[1] = {z};
+    double chance[1];
+    of(one, e, chance);
+    return chance[0];
+  }
+  // Whether one of the tokens may have a chance.
+  template <int N>
+  __device__ __forceinline__ bool any(const float (&z)[N], int e0) const {
+    if (state == kOneToken) return e0 <= upto && upto < e0 + N;
+    float most = z[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) most = fmaxf(most, z[k]);
+    return most >= cut;
   }
 };
 
@@ -276,11 +302,20 @@ struct Rest {
         p(v.p),
         q(v.q),
         certain(v.certain) {}
-  __device__ __forceinline__ double of(float z, float y, int e) const {
+  // What is left of N tokens with logits z and y from e0 on.
+  template <int N>
+  __device__ __forceinline__ void of(const float (&z)[N], const float (&y)[N], int e0, double (&left)[N]) const {
 #pragma clang fp contract(off)
-    const double chance = p.of(z, e);
-    if (zq) return fmax(chance - q.of(y, e), 0.0);  // uniform
-    return e == certain ? 0.0 : chance;
+    p.of(z, e0, left);
+    if (zq) {
+      double own[N];
+      q.of(y, e0, own);
+#pragma unroll
+      for (int k = 0; k < N; ++k) left[k] = fmax(left[k] - own[k], 0.0);
+    } else if (certain >= 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) left[k] = e0 + k == certain ? 0.0 : left[k];
+    }
   }
 };
 
@@ -308,18 +343,23 @@ struct RestBlock {
 #pragma unroll
       for (int c = 0; c < 2; ++c) y[c] = load8(rest.zq, first(b, lane, c), V);
   }
-  // The sum of the block's chances, in each of its 16 lanes.
-  __device__ __forceinline__ double sum(const Rest<T>& rest, int b, int lane) const {
+  // The sum of the block's chances, in each of its 16 lanes. (One copy of the
+  // code for both halves: the registers move on.)
+  __device__ __forceinline__ double sum(const Rest<T>& rest, int b, int lane) {
     double s = 0.0;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 2; ++c) {
       const int e0 = first(b, lane, c);
-      bool any = false;
+      float zf[kChunk], yf[kChunk];
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) any |= rest.p.kept((float)z[c][k], e0 + k);
-      if (!__any(any)) continue;  // most of a row with limits
+      for (int k = 0; k < kChunk; ++k) zf[k] = (float)z[0][k], yf[k] = (float)y[0][k];
+      z[0] = z[1];
+      y[0] = y[1];
+      if (!__any(rest.p.any(zf, e0))) continue;  // most of a row with limits
+      double left[kChunk];
+      rest.of(zf, yf, e0, left);
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) s += rest.of((float)z[c][k], (float)y[c][k], e0 + k);  // 0 past the row's end
+      for (int k = 0; k < kChunk; ++k) s += left[k];  // 0 past the row's end
     }
     return row_reduce(s, Add());
   }
@@ -370,7 +410,7 @@ __global__ __launch_bounds__(kRestThreads) void verify_rest_kernel(VerifyArgs a,
   next.load(rest, b, lane, a.V);
 #pragma unroll 1
   for (;;) {
-    const RestBlock<T> now = next;
+    RestBlock<T> now = next;
     const int then = b + kRestBlocks;
     if (then < end) next.load(rest, then, lane, a.V);
     const double s = now.sum(rest, b, lane);
@@ -405,14 +445,13 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int block
     sh.first = 0x7fffffff;
     sh.last = -1;
   }
-  if (v.state == kNoRow) {
-    if (threadIdx.x == 0) {
-      a.tokens[at] = -1;
-      if (a.logp) a.logp[at] = NAN;
-      if (a.kept_logp) a.kept_logp[at] = NAN;
-    }
-    return;
-  }
+  const auto none = [&] {
+    if (threadIdx.x > 0) return;
+    a.tokens[at] = -1;
+    if (a.logp) a.logp[at] = NAN;
+    if (a.kept_logp) a.kept_logp[at] = NAN;
+  };
+  if (v.state == kNoRow) return none();
   Rest<T> rest(a, seq, v);
   double* sums = a.rest + seq * blocks;
   const int each = (blocks + NT - 1) / NT;
@@ -452,6 +491,7 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int block
   say_ends(sh, first, last);
   __syncthreads();
   const int block = uniform(sh.first < 0x7fffffff ? sh.first : sh.last);
+  if (block < 0) return none();  // no block holds anything: a row with a distribution has one that does
   if (block >= b0 && block < b1) {
     run = before;
     for (int b = b0; b < block; ++b) run += sums[b];
@@ -465,13 +505,18 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int block
   float z = 0.f;
   if (threadIdx.x < kSampleBlock && e < a.V) {
     z = (float)rest.zp[e];
-    r = rest.of(z, rest.zq ? (float)rest.zq[e] : 0.f, e);
+    const float one[1] = {z}, other[1] = {rest.zq ? (float)rest.zq[e] : 0.f};
+    double left[1];
+    rest.of(one, other, e, left);
+    r = left[0];
   }
   double all;
   const double upto = block_scan(r, sh.scan, all) + r;  // its barriers are after the resets
   say_ends(sh, r > 0.0 && upto > inside ? e : 0x7fffffff, r > 0.0 ? e : -1);
   __syncthreads();
-  if (e == (sh.first < 0x7fffffff ? sh.first : sh.last) && threadIdx.x < kSampleBlock) {
+  const int token = uniform(sh.first < 0x7fffffff ? sh.first : sh.last);
+  if (token < 0) return none();
+  if (e == token && threadIdx.x < kSampleBlock) {
     const VerifyRow& row = v.p;
     float lp = 0.f, kp = 0.f;
     if (row.state == kWeights) {
