@@ -189,6 +189,7 @@ def test_full_vocabulary():
         check(z, tokens, u, q, target=s, drafts=s)
     z, tokens, u, q = inputs(2, 1, 1 << 20, "bf16", 2)
     check(z, tokens, u, q)
+    check(z, tokens, u, q, target=dict(top_k=100, top_p=0.95), drafts=dict(top_p=0.9))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -365,6 +366,21 @@ def test_many_rows_and_many_drafts():
     u = 0.99 * torch.rand(B, K + 1, generator=g)
     r = check(z, tokens, u, q)
     assert (r["accepted"] > 256).any()  # past what one workgroup looks at in a step
+
+
+@pytest.mark.parametrize("certain", [False, True])
+def test_batches_that_leave_rows_out(certain):
+    """So many rows with limits that those after a refused draft are left out, in
+    an order that changes with the launch: the same bits at every call."""
+    require_gpu()
+    B, K, V = 300, 4, 1500
+    z, tokens, u, q = inputs(B, K, V, "bf16", 77, certain=certain)
+    n = torch.randint(0, K + 1, (B,), generator=torch.Generator().manual_seed(1)).int()
+    for s in (dict(top_p=0.9), dict(top_k=20, temperature=0.7)):
+        first = check(z, tokens, u, q, n, s, s)
+        for _ in range(4):
+            again = check(z, tokens, u, q, n, s, s)
+            assert all(torch.equal(first[k], again[k]) for k in first)
 
 
 def test_offsets_past_32_bits():
