@@ -57,7 +57,8 @@ struct VerifyArgs {
   double* rest;
   int64_t B;
   int K, V, dtype;
-  int skip;  // whether rows look at `refused`
+  int skip;  // whether rows look at `refused`, and go by their place in the sequence
+  int slot;  // then the first place of a launch: a target's row and its draft's are two places
 };
 constexpr int kVerifyMaxK = 1024;
 inline int verify_rows(int K, bool drafts) { return K + 1 + (drafts ? K : 0); }

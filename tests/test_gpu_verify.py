@@ -373,14 +373,14 @@ def test_batches_that_leave_rows_out(certain):
     """So many rows with limits that those after a refused draft are left out, in
     an order that changes with the launch: the same bits at every call."""
     require_gpu()
-    B, K, V = 300, 4, 1500
-    z, tokens, u, q = inputs(B, K, V, "bf16", 77, certain=certain)
-    n = torch.randint(0, K + 1, (B,), generator=torch.Generator().manual_seed(1)).int()
-    for s in (dict(top_p=0.9), dict(top_k=20, temperature=0.7)):
-        first = check(z, tokens, u, q, n, s, s)
-        for _ in range(4):
-            again = check(z, tokens, u, q, n, s, s)
-            assert all(torch.equal(first[k], again[k]) for k in first)
+    for B, K, V in ((300, 4, 1500), (700, 3, 600)):
+        z, tokens, u, q = inputs(B, K, V, "bf16", 77, certain=certain)
+        n = torch.randint(0, K + 1, (B,), generator=torch.Generator().manual_seed(1)).int()
+        for s in (dict(top_p=0.9), dict(top_k=20, temperature=0.7)):
+            first = check(z, tokens, u, q, n, s, s)
+            for _ in range(3):
+                again = check(z, tokens, u, q, n, s, s)
+                assert all(torch.equal(first[k], again[k]) for k in first)
 
 
 def test_offsets_past_32_bits():
