@@ -32,6 +32,8 @@ struct VecOf {
   typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
 
+typedef unsigned __int128 Bits;
+
 // Elements d .. d + V - 1 of a row of H, those past its end as 0.
 template <typename T, int V, bool STREAM = false>
 __device__ __forceinline__ typename VecOf<T, V>::type load_raw(const T* row, int d, int H) {
@@ -42,6 +44,12 @@ __device__ __forceinline__ typename VecOf<T, V>::type load_raw(const T* row, int
     else
       return *reinterpret_cast<const TV*>(row + d);
   }
+  if constexpr (sizeof(TV) == sizeof(Bits))
+    if (H >= V) {  // the end of the row's last 16 bytes
+      const Bits b = __builtin_bit_cast(Bits, *reinterpret_cast<const TV*>(row + H - V));
+      const int past = d + V - H;  // elements; the whole of it where d is past the row
+      return __builtin_bit_cast(TV, past < V ? (Bits)(b >> 8 * (int)sizeof(T) * past) : (Bits)0);
+    }
   TV t = {};
 #pragma unroll
   for (int k = 0; k < V; ++k)
@@ -173,6 +181,7 @@ __global__ __launch_bounds__(256) void sort_counting_kernel(const int64_t* __res
 }
 
 constexpr int kMinBits = 8, kMaxBits = 10;
+constexpr int kHeld = 2;
 constexpr int kRadixWaves = 8, kRadixThreads = kRadixWaves * 64;
 
 struct RadixPass {
@@ -214,9 +223,13 @@ __global__ __launch_bounds__(kRadixThreads) void radix_move_kernel(RadixPass a, 
   const int64_t begin = blockIdx.x * a.per, end = begin + a.per < a.N ? begin + a.per : a.N;
   const int64_t each = (a.per + kRadixWaves - 1) / kRadixWaves;
   const int64_t w0 = begin + wave * each < end ? begin + wave * each : end, w1 = w0 + each < end ? w0 + each : end;
-  for (int d = threadIdx.x; d < kRadixWaves * digits; d += kRadixThreads) at[d / digits][d % digits] = 0;
-  __syncthreads();
-  for (int64_t i = w0 + lane; i < w1; i += 64) atomicAdd(&at[wave][a.key_at(i) >> a.shift & (digits - 1)], 1u);
+  // the first tokens of each wave, which are all of them in a batch of up to 256 K, stay in registers
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int64_t i = w0 + k * 64 + lane;
+    held[k] = i < w1 ? a.key_at(i) : 0;
+  }
   // where each digit begins in this workgroup: all smaller digits, and the same in the workgroups before.
   // Four digits a load, the workgroups' counts shared out to the threads.
   const int quads = digits / 4, subsets = kRadixThreads / quads, quad = (int)threadIdx.x % quads;
@@ -228,6 +241,12 @@ __global__ __launch_bounds__(kRadixThreads) void radix_move_kernel(RadixPass a, 
     all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
     prior.x += c.x & here, prior.y += c.y & here, prior.z += c.z & here, prior.w += c.w & here;
   }
+  for (int d = threadIdx.x; d < kRadixWaves * digits; d += kRadixThreads) at[d / digits][d % digits] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (w0 + k * 64 + lane < w1) atomicAdd(&at[wave][held[k] >> a.shift & (digits - 1)], 1u);
+  for (int64_t i = w0 + kHeld * 64 + lane; i < w1; i += 64) atomicAdd(&at[wave][a.key_at(i) >> a.shift & (digits - 1)], 1u);
   reinterpret_cast<uint4*>(part_all)[threadIdx.x] = all;
   reinterpret_cast<uint4*>(part_prior)[threadIdx.x] = prior;
   __syncthreads();  // the waves' counts are whole, too
@@ -264,10 +283,17 @@ __global__ __launch_bounds__(kRadixThreads) void radix_move_kernel(RadixPass a, 
     }
   }
   __syncthreads();
-  for (int64_t i0 = w0; i0 < w1; i0 += 64) {
+  int step = 0;
+  for (int64_t i0 = w0; i0 < w1; i0 += 64, ++step) {
     const int64_t i = i0 + lane;
     const bool in = i < w1;
-    const uint32_t key = in ? a.key_at(i) : 0;
+    uint32_t key = 0;
+    if (step < kHeld) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) key = step == k ? held[k] : key;
+    } else if (in) {
+      key = a.key_at(i);
+    }
     const uint32_t pos = in ? (a.tokens ? (uint32_t)i : a.pos[i]) : 0;
     const uint32_t digit = key >> a.shift & (digits - 1);
     uint64_t same = __ballot(in);
@@ -367,7 +393,7 @@ __global__ __launch_bounds__(kAddWaves * 64) void embed_add_kernel(EmbedBwd a, c
   TW* const w = (TW*)a.grad_weight;
   const auto end_row = [&](const WV& old) {  // of row v
     if (v == v0) {
-      if (in) store_part<float, V>(a.head + range * a.H, d, a.H, sum);
+      if (in) store_part<float, V>(a.head + range * part_width(a.H), d, part_width(a.H), sum);
       headed = true;
     } else if (in) {
       float x[V];
@@ -424,7 +450,7 @@ __global__ __launch_bounds__(kAddWaves * 64) void embed_add_kernel(EmbedBwd a, c
     if (done) break;
   }
   if (any && !to.shared) end_row(before);
-  if (any && in) store_part<float, V>(a.tail + range * a.H, d, a.H, sum);
+  if (any && in) store_part<float, V>(a.tail + range * part_width(a.H), d, part_width(a.H), sum);
   if (slice == 0 && lane == 0) {
     a.tail_row[range] = any ? v : -1;
     // listed in any order: each is added up by itself
@@ -468,7 +494,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embed_join_kernel(EmbedBwd a,
 #pragma unroll 8
       for (int64_t k = from; k < to; ++k) {
         float x[V];
-        load_part<float, V>(a.tail + k * a.H, d, a.H, x);
+        load_part<float, V>(a.tail + k * part_width(a.H), d, part_width(a.H), x);
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] += x[e];
       }
@@ -478,7 +504,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void embed_join_kernel(EmbedBwd a,
     if (wave == 0 && d < a.H) {
       TW* const w = (TW*)a.grad_weight + (int64_t)row * a.H;
       float x[V], old[V] = {};
-      load_part<float, V>(a.head + range * a.H, d, a.H, x);
+      load_part<float, V>(a.head + range * part_width(a.H), d, part_width(a.H), x);
       if constexpr (ACC) load_part<TW, V>(w, d, a.H, old);
       for (int p = 1; p < kJoinWaves; ++p)
 #pragma unroll
@@ -551,9 +577,12 @@ EmbedBwdPlan embed_bwd_plan(int64_t N, int H, int V, int grad_y_dtype) {
   p.blocks = (int)std::min<int64_t>(256, (N + 1023) / 1024);
   p.per = p.blocks ? (N + p.blocks - 1) / p.blocks : 0;
   p.slices = slices_of(H, grad_y_dtype);
-  // some 8192 waves, about what runs at once
+  // some 8192 waves, about what runs at once, but no range of fewer than the
+  // tokens that are loaded together (16384 of 896 bf16, into the head's: 41 us,
+  // 46 with ranges of 4), or half of that for the few that are sorted by
+  // counting (512: 14.2 with 4, 15.0 with 8, 14.6 with 1)
   const int64_t most = std::max<int64_t>(1, 8192 / p.slices);
-  p.items = (int)std::max<int64_t>(1, (N + most - 1) / most);
+  p.items = (int)std::max<int64_t>(p.radix ? kBatch : kBatch / 2, (N + most - 1) / most);
   p.ranges = (N + p.items - 1) / p.items;
   p.shared = N > kShared;  // a row has kShared tokens past a range's end, and one before
   return p;

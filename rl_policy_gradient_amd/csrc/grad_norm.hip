@@ -62,11 +62,13 @@ __device__ __forceinline__ Tile tile_of(const GradLaunch& a, uint32_t b) {
   return t;
 }
 
-template <typename T>
-__device__ __forceinline__ double squares(const T* p, int64_t n) {
+// The squares of n elements that thread `thread` of `threads` takes, `deep`
+// loads of it in flight.
+template <int deep, typename T>
+__device__ __forceinline__ double squares(const T* p, int64_t n, int thread, int threads) {
   typedef typename Vec<T>::type TV;
   constexpr int V = vec_of<T>;
-  constexpr int64_t step = (int64_t)NT * V;
+  const int64_t step = (int64_t)threads * V;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
   const auto add = [&](const TV& x) {
 #pragma unroll
@@ -75,13 +77,13 @@ __device__ __forceinline__ double squares(const T* p, int64_t n) {
       s[k % 4] = fma(g, g, s[k % 4]);
     }
   };
-  int64_t i = (int64_t)threadIdx.x * V;
-  for (; i + 3 * step + V <= n; i += 4 * step) {
-    TV x[4];
+  int64_t i = (int64_t)thread * V;
+  for (; i + (deep - 1) * step + V <= n; i += deep * step) {
+    TV x[deep];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const TV*>(p + i + c * step);
+    for (int c = 0; c < deep; ++c) x[c] = *reinterpret_cast<const TV*>(p + i + c * step);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) add(x[c]);
+    for (int c = 0; c < deep; ++c) add(x[c]);
   }
   for (; i + V <= n; i += step) add(*reinterpret_cast<const TV*>(p + i));
   for (; i < n; ++i) {  // fewer than V, of one thread
@@ -90,20 +92,32 @@ __device__ __forceinline__ double squares(const T* p, int64_t n) {
   }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
+template <int deep>
+__device__ __forceinline__ double squares_of(const GradLaunch& a, const Tile& t, int thread, int threads) {
+  return t.bf16 ? squares<deep>((const __bf16*)a.t[t.e].p + t.begin, t.n, thread, threads)
+                : squares<deep>((const float*)a.t[t.e].p + t.begin, t.n, thread, threads);
+}
 
 __global__ __launch_bounds__(NT) void grad_squares_kernel(const GradLaunch a, double* __restrict__ part,
                                                           uint32_t* __restrict__ start) {
   __shared__ double red[NT / 64];
   const uint32_t b = blockIdx.x;
   const Tile t = tile_of(a, b);
-  double s = t.bf16 ? squares((const __bf16*)a.t[t.e].p + t.begin, t.n) : squares((const float*)a.t[t.e].p + t.begin, t.n);
-  s = wave_sum(s);
+  const double s = wave_sum(squares_of<4>(a, t, threadIdx.x, NT));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     part[a.first_tile + b] = (red[0] + red[1]) + (red[2] + red[3]);
     if (t.begin == 0) start[a.first_tensor + t.e] = a.first_tile + b;
   }
+}
+
+// The norm of a sum of squares, and the factor that goes with it.
+__device__ __forceinline__ void say_norm(const GradFinish& a, double given, double sum) {
+  const double norm = fabs(given) * sqrt(sum);
+  const float n32 = (float)norm;
+  a.norm[0] = n32;
+  a.scale[0] = fabsf(n32) < INFINITY ? (float)(given * fmin(1.0, a.max_norm / (norm + a.eps))) : NAN;
 }
 
 // Workgroup 0 the whole norm, the others a tensor's each.
@@ -124,13 +138,39 @@ __global__ __launch_bounds__(NT) void grad_finish_kernel(const GradFinish a) {
   __syncthreads();
   if (threadIdx.x > 0) return;
   s = (red[0] + red[1]) + (red[2] + red[3]);
-  const double norm = fabs(given) * sqrt(s);
-  const float n32 = (float)norm;
-  if (blockIdx.x > 0) {
-    a.norms[i] = n32;
-  } else {
-    a.norm[0] = n32;
-    a.scale[0] = fabsf(n32) < INFINITY ? (float)(given * fmin(1.0, a.max_norm / (norm + a.eps))) : NAN;
+  if (blockIdx.x > 0)
+    a.norms[i] = (float)(fabs(given) * sqrt(s));
+  else
+    say_norm(a, given, s);
+}
+
+// A short list at once: one workgroup, a wave a tile at a time.
+constexpr int kSmallThreads = 1024;
+__global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(const GradLaunch a, const GradFinish f) {
+  __shared__ double part[kGradSmallTiles];
+  __shared__ uint32_t start[kGradMaxTensors + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (uint32_t b = wave; b < a.groups; b += kSmallThreads / 64) {
+    const Tile t = tile_of(a, b);
+    const double s = wave_sum(squares_of<8>(a, t, lane, 64));
+    if (lane == 0) {
+      part[b] = s;
+      if (t.begin == 0) start[t.e] = b;
+    }
+  }
+  if (threadIdx.x == 0) start[a.count] = a.groups;
+  __syncthreads();
+  const double given = f.grad_scale ? (double)*f.grad_scale : 1.0;
+  if (f.norms && threadIdx.x < a.count) {
+    double s = 0.0;
+    for (uint32_t k = start[threadIdx.x]; k < start[threadIdx.x + 1]; ++k) s += part[k];
+    f.norms[threadIdx.x] = (float)(fabs(given) * sqrt(s));
+  }
+  if (wave == kSmallThreads / 64 - 1) {
+    double s = 0.0;
+    for (uint32_t k = lane; k < a.groups; k += 64) s += part[k];
+    s = wave_sum(s);
+    if (lane == 0) say_norm(f, given, s);
   }
 }
 
@@ -175,6 +215,11 @@ hipError_t launch_grad_squares(const GradLaunch& a, double* part, uint32_t* star
 
 hipError_t launch_grad_finish(const GradFinish& a, hipStream_t st) {
   grad_finish_kernel<<<1 + (a.norms ? a.count : 0), NT, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_small(const GradLaunch& a, const GradFinish& f, hipStream_t st) {
+  grad_small_kernel<<<1, kSmallThreads, 0, st>>>(a, f);
   return hipGetLastError();
 }
 

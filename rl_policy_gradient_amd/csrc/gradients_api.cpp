@@ -37,8 +37,8 @@ size_t carve_embed_bwd(void* ws, EmbedBwd& a) {
   a.tail_row = c.take<int32_t>((size_t)p.ranges);
   a.shared_rows = c.take<uint32_t>(1);
   a.shared_list = c.take<uint2>((size_t)p.ranges);
-  a.head = c.take<float>((size_t)p.ranges * a.H);
-  a.tail = c.take<float>((size_t)p.ranges * a.H);
+  a.head = c.take<float>((size_t)p.ranges * part_width(a.H));
+  a.tail = c.take<float>((size_t)p.ranges * part_width(a.H));
   return c.off;
 }
 
@@ -49,6 +49,10 @@ constexpr int kMaxGrads = 1 << 20;
 // bf16), and at most some 4096 tiles for the finishing workgroup to add.
 constexpr int kMinTileShift = 11;
 constexpr int64_t kMostTiles = 4096;
+
+// Elements of a list whose norm one workgroup forms in one launch.
+constexpr int64_t kSmallTotal = (int64_t)1 << 17;
+static_assert((kSmallTotal >> kMinTileShift) + kGradMaxTensors <= kGradSmallTiles, "a list's tiles fit");
 
 int check_grads(const plp_grad_tensor* t, int32_t count, int64_t* total) {
   if (count < 0 || count > kMaxGrads || (count > 0 && !t))
@@ -217,11 +221,6 @@ PLP_API int plp_grad_norm(const plp_grad_tensor* tensors, int32_t count, double 
   if (rc) return rc;
   rc = check_ws(ws, ws_bytes, need);
   if (rc) return rc;
-  rc = for_launches(tensors, count, shift, [&](const GradLaunch& l) {
-    HIP_TRY(launch_grad_squares(l, w.part, w.start, st));
-    return (int)PLP_OK;
-  });
-  if (rc) return rc;
   GradFinish f;
   f.part = w.part;
   f.start = w.start;
@@ -233,6 +232,18 @@ PLP_API int plp_grad_norm(const plp_grad_tensor* tensors, int32_t count, double 
   f.eps = eps;
   f.tiles = (uint32_t)tiles;
   f.count = (uint32_t)count;
+  if (count > 0 && count <= kGradMaxTensors && total <= kSmallTotal) {
+    rc = for_launches(tensors, count, shift, [&](const GradLaunch& l) {
+      HIP_TRY(launch_grad_small(l, f, st));
+      return (int)PLP_OK;
+    });
+    return rc ? rc : ok();
+  }
+  rc = for_launches(tensors, count, shift, [&](const GradLaunch& l) {
+    HIP_TRY(launch_grad_squares(l, w.part, w.start, st));
+    return (int)PLP_OK;
+  });
+  if (rc) return rc;
   HIP_TRY(launch_grad_finish(f, st));
   return ok();
 }

@@ -17,7 +17,7 @@ struct GradEntry {
 };
 // Tensors of one launch: the table goes by value in the kernel's arguments,
 // which hold 4 KB.
-constexpr int kGradMaxTensors = 250;
+constexpr int kGradMaxTensors = 240;
 struct GradLaunch {
   GradEntry t[kGradMaxTensors];
   uint32_t count, groups;   // tensors, workgroups
@@ -25,7 +25,6 @@ struct GradLaunch {
   uint32_t first_tensor;    // of the whole list
   uint32_t first_tile;      // this launch's first workgroup among all launches'
 };
-static_assert(sizeof(GradLaunch) + 32 <= 4096, "kernel arguments");
 
 // The sums of squares: one double a tile into part, the tile each tensor begins
 // at into start.
@@ -38,7 +37,12 @@ struct GradFinish {
   double max_norm, eps;
   uint32_t tiles, count;
 };
+static_assert(sizeof(GradLaunch) + sizeof(GradFinish) <= 4096, "kernel arguments");
 hipError_t launch_grad_finish(const GradFinish& a, hipStream_t st);
+// Both in one launch of one workgroup, for lists of one launch and up to so
+// many tiles.
+constexpr int kGradSmallTiles = 64 + kGradMaxTensors;
+hipError_t launch_grad_small(const GradLaunch& a, const GradFinish& f, hipStream_t st);
 // g = round(g scale), unless scale is 1 or not finite.
 hipError_t launch_grad_clip(const GradLaunch& a, const float* scale, hipStream_t st);
 
@@ -66,6 +70,8 @@ struct EmbedBwdPlan {
   bool shared;       // whether ranges can share a row
 };
 EmbedBwdPlan embed_bwd_plan(int64_t N, int H, int V, int grad_y_dtype);
+// Columns of a partial sum: whole vectors, so that none is cut at a row's end.
+__host__ __device__ inline int part_width(int H) { return (H + 7) / 8 * 8; }
 struct EmbedBwd {
   const int64_t* tokens;
   const void* grad_y;
@@ -76,7 +82,7 @@ struct EmbedBwd {
   // workspace
   uint32_t *key[2], *pos[2];    // [N] each; the second pair with radix passes only
   uint32_t* hist;               // [blocks][1 << bits], with radix passes only
-  float *head, *tail;           // [ranges][H] partial sums of rows that ranges share: of the range they
+  float *head, *tail;           // [ranges][part_width(H)] partial sums of rows that ranges share: of the range they
                                 // end in, and of those before
   int32_t* tail_row;            // [ranges] the row that tail is of, or -1
   uint32_t* shared_rows;        // how many ranges have a head

@@ -153,7 +153,8 @@ def grad_norm(grads: Union[GradTable, Sequence[torch.Tensor]], *, max_norm: Opti
         _one_device((("workspace", workspace), ("gradients", table.grads[0])))
     limit = math.inf if max_norm is None else float(max_norm)
     with _on(dev):
-        res = {"norm": _out(out, "norm", (1,), torch.float32, dev), "scale": _out(out, "scale", (1,), torch.float32, dev)}
+        norm = _out(out, "norm", (1,), torch.float32, dev, grad_scale if grad_scale is not None and grad_scale.dim() == 1 else None)
+        res = {"norm": norm, "scale": _out(out, "scale", (1,), torch.float32, dev, norm)}
         if norms:
             res["norms"] = _out(out, "norms", (table.count,), torch.float32, dev)
         ws = _workspace(table._bytes, dev, workspace)

@@ -43,7 +43,7 @@ int main() {
                   PLP_E_INVALID);
           }
   // lists around the ends of a launch and of a tile, whose tables are made before the workspace is looked at
-  for (int count : {0, 1, 249, 250, 251, 501, 5000})
+  for (int count : {0, 1, 239, 240, 241, 501, 5000})
     for (int64_t numel : {(int64_t)0, (int64_t)1, (int64_t)2047, (int64_t)2049, (int64_t)1 << 27}) {
       std::vector<plp_grad_tensor> t(count);
       for (int i = 0; i < count; ++i) t[i] = plp_grad_tensor{at(0), numel + i % 3, i % 2, 0};
