@@ -16,6 +16,17 @@
 // Adding: a wave takes a range of the sorted tokens, for 64 lanes' columns. A
 // row whose tokens go on past a range's end by a few is finished there, else it
 // is left in parts, which a last kernel adds up in their order.
+//
+// What bounds them. Forward: HBM, 25 us for 65536 rows of 896 bf16 (6.0 TB/s
+// with the tables' rows that the tokens name read once). Backward of as many
+// into 151936 x 896 bf16, 85 us: the zeros 46 (5.9 TB/s, the sort beside them),
+// 32 to read the rows in the tokens' order and write the 15 000 that have any
+// (4.2 TB/s: 16 rows of a range are two loads of eight), 9 for the rows that
+// ranges share (the commonest token's 3300 rows are some 200 parts). One pass
+// that wrote every row once, zeros where a merge of tokens and rows had none,
+// took 108: the sort, which only latency bounds, came before all of it. 16384
+// rows of 4096 fp32 into 32000: 150 (5.3 TB/s). Into a gradient that is there:
+// 512 rows 14 (the call from Python; 3.6, 7.1 and 3.6 on the device), 65536 70.
 #include "training_ops.h"
 
 #include <algorithm>
@@ -87,6 +98,9 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // takes 25 us so and 33 otherwise, with a norm of its rows after it 73 and 78;
 // of 32768 rows 18.5 and 19.5, but with the norm 41 and 38.
 constexpr int64_t kStreamBytes = (int64_t)1 << 26;
+// Threads that set grad_weight to zero, two waves a CU: with 2^14 of them the
+// backward of 65536 rows of 896 takes 112 us, with 2^15 86, 2^16 89, 2^17 95 and
+// 2^19, as many as run at once, 98.
 constexpr int kFillThreads = 1 << 15;
 
 // ---- forward -----------------------------------------------------------------

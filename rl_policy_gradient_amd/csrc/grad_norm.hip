@@ -8,8 +8,15 @@
 // Squares are formed and added in fp64: a square of an fp32 or bf16 value is
 // exact there (24 + 24 bits of 53) and neither over- nor underflows, so a norm
 // is good to half a step of fp32 whatever the gradients' size. Two launches: a
-// workgroup a tile leaves the tile's sum, then one workgroup adds the tiles'
-// sums in a fixed order (and others those of each tensor, where asked for).
+// workgroup a tile (at most some 4096 in all) leaves the tile's sum, then one
+// workgroup adds the tiles' sums in a fixed order, and others those of a tensor
+// each, where asked for. A short list takes one launch of one workgroup.
+//
+// Bound by HBM: 145 tensors of 367 million bf16 elements take 126 us (5.8 TB/s,
+// two operations in fp64 an element are 20 us of that at their rate) and 4 to
+// finish; 27 million, which the caches after the L2 hold, 12.4 (4.4 TB/s) and 4,
+// and their clipping in place 18.6 (5.8 TB/s, read and written). Finishing took
+// 10 where a wave added up a tensor, the head's 2000 tiles among them.
 #include "training_ops.h"
 
 #include <math.h>
@@ -144,7 +151,8 @@ __global__ __launch_bounds__(NT) void grad_finish_kernel(const GradFinish a) {
     say_norm(a, given, s);
 }
 
-// A short list at once: one workgroup, a wave a tile at a time.
+// A short list at once: one workgroup, a wave a tile at a time (a dozen tensors
+// of 98 000 fp32 elements: 6.8 us).
 constexpr int kSmallThreads = 1024;
 __global__ __launch_bounds__(kSmallThreads) void grad_small_kernel(const GradLaunch a, const GradFinish f) {
   __shared__ double part[kGradSmallTiles];

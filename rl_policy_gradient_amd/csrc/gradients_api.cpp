@@ -50,9 +50,11 @@ constexpr int kMaxGrads = 1 << 20;
 constexpr int kMinTileShift = 11;
 constexpr int64_t kMostTiles = 4096;
 
-// Elements of a list whose norm one workgroup forms in one launch.
+// Elements and tiles of a list whose norm one workgroup forms in one launch. A
+// call from Python takes 9 to 11 us so, and 12 to 14 in two launches, whose time
+// on the host is what counts there; of 100 tensors 12 and 15, but of 200 it is
+// the one workgroup that counts, 21 and 19.
 constexpr int64_t kSmallTotal = (int64_t)1 << 17;
-static_assert((kSmallTotal >> kMinTileShift) + kGradMaxTensors <= kGradSmallTiles, "a list's tiles fit");
 
 int check_grads(const plp_grad_tensor* t, int32_t count, int64_t* total) {
   if (count < 0 || count > kMaxGrads || (count > 0 && !t))
@@ -232,7 +234,7 @@ PLP_API int plp_grad_norm(const plp_grad_tensor* tensors, int32_t count, double 
   f.eps = eps;
   f.tiles = (uint32_t)tiles;
   f.count = (uint32_t)count;
-  if (count > 0 && count <= kGradMaxTensors && total <= kSmallTotal) {
+  if (count > 0 && tiles <= kGradSmallTiles && total <= kSmallTotal) {
     rc = for_launches(tensors, count, shift, [&](const GradLaunch& l) {
       HIP_TRY(launch_grad_small(l, f, st));
       return (int)PLP_OK;

@@ -39,9 +39,9 @@ struct GradFinish {
 };
 static_assert(sizeof(GradLaunch) + sizeof(GradFinish) <= 4096, "kernel arguments");
 hipError_t launch_grad_finish(const GradFinish& a, hipStream_t st);
-// Both in one launch of one workgroup, for lists of one launch and up to so
-// many tiles.
-constexpr int kGradSmallTiles = 64 + kGradMaxTensors;
+// Both in one launch of one workgroup, for lists of up to so many tiles.
+constexpr int kGradSmallTiles = 128;
+static_assert(kGradSmallTiles <= kGradMaxTensors, "a tensor has a tile: such a list goes in one launch");
 hipError_t launch_grad_small(const GradLaunch& a, const GradFinish& f, hipStream_t st);
 // g = round(g scale), unless scale is 1 or not finite.
 hipError_t launch_grad_clip(const GradLaunch& a, const float* scale, hipStream_t st);

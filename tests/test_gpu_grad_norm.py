@@ -85,12 +85,12 @@ def test_many_tensors(count):
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("more", [-1, 0, 1])
 def test_around_what_one_workgroup_takes(more, kind):
-    """Lists of about 2^17 elements and 240 tensors, which go in one launch up to there."""
+    """Lists of about 2^17 elements and 128 tiles, which go in one launch up to there."""
     require_gpu()
     check(some([(1 << 17) - 5000 + more, 4000, 0, 1000], [kind] * 4, 1), max_norm=0.1)
     g = torch.Generator().manual_seed(3)
-    check(some(torch.randint(0, 1000, (240 + more,), generator=g).tolist(), ["f32", "bf16"] * 121, 2), max_norm=0.1)
-    check(some([2048] * 64 + [1] * (more + 1), [kind] * 66, 4), max_norm=0.1)
+    check(some(torch.randint(0, 1000, (128 + more,), generator=g).tolist(), ["f32", "bf16"] * 65, 2), max_norm=0.1)
+    check(some([2048] * 63 + [1] * (65 + more), [kind] * 130, 4), max_norm=0.1)
 
 
 def test_sizes_of_the_range():
