@@ -98,8 +98,10 @@ def test_of_nothing_and_workspace():
                 for drafts in (0, 1):
                     assert L.plp_verify_tokens_workspace_size(B, K, V, drafts, ctypes.byref(n)) == abi.PLP_OK
                     rows, blocks = B * (K + 1 + (K if drafts else 0)), (V + 255) // 256
-                    least = rows * (blocks * 12 + 40) + B * (blocks * 8 + 12)
-                    assert n.value % 256 == 0 and least <= n.value <= least + rows * 12 + 5 * 256
+                    # 12 bytes a block and 40 a row; a sequence's two chances a draft, verdict, mark and blocks' sums
+                    least = rows * (blocks * 12 + 40) + B * (16 * K + 112 + 4 + blocks * 8)
+                    # a row may begin within a block of 256: up to one more
+                    assert n.value % 256 == 0 and least <= n.value <= least + rows * 12 + 7 * 256
     assert L.plp_verify_tokens_workspace_size(1, 1, 1, 0, None) == abi.PLP_E_INVALID
     assert L.plp_verify_tokens_workspace_size(1, 2000, 1, 0, ctypes.byref(n)) == abi.PLP_E_UNSUPPORTED
 
