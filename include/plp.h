@@ -316,9 +316,9 @@ PLP_API int plp_policy_loss_from_logprobs(const plp_args* args, const float* log
 
 /* ---- Operators around the fused loss ---------------------------------------
  * The other calls of a policy's training loop: sampling the completions (the
- * targets and their old_logp), the final norm that gives `hidden` and takes
- * grad_hidden back, the AdamW step that takes grad_weight and grad_bias, the
- * embedding and its gradient, and the norm of all gradients.
+ * targets and their old_logp) or verifying drafted ones, the embedding and the
+ * final norm (whose output is `hidden`) with their gradients, the norm of all
+ * gradients, and the AdamW step that takes grad_weight and grad_bias.
  * They follow the conventions above, but for alignment: a tensor needs only
  * the alignment of its elements. Outputs that share memory with an input or
  * with each other are refused (PLP_E_INVALID). These entry points were added
@@ -485,12 +485,12 @@ typedef struct plp_verify_args {
  * after the last accepted one is drawn from max(0, p_k - q_k) where draft k was
  * refused, and from p_n after all n of them were accepted: the first index at
  * which the running sum exceeds the last uniform times the sum. Each token is
- * then distributed as one drawn from p. (Where p_k - q_k is nowhere above
- * zero, as for a draft that neither side could give, it is drawn from p_k.) A draft outside [0,V) is refused. Rows past
- * the sequence's num_drafts are not read. Probabilities are formed in 64 bits,
- * good to about 1e-13 of themselves (one below 2^-1000 of the row's largest is
- * 0); sums in an order that goes by V, so a
- * sequence's result does not depend on the others, and on its place in memory
+ * then distributed as one drawn from p. (Where p_k - q_k is nowhere above zero,
+ * as for a draft that neither side could give, it is drawn from p_k.) A draft
+ * outside [0,V) is refused. Rows past the sequence's num_drafts are not read.
+ * Probabilities are formed in 64 bits, good to about 1e-13 of themselves (one
+ * below 2^-1000 of the row's largest is 0); sums in an order that goes by V, so
+ * a sequence's result does not depend on the others, and on its place in memory
  * only where a border lies within that of a uniform. A sequence that comes to a
  * row without a distribution (plp_sample_tokens says which; the target's, or the
  * draft's of a draft that all before were accepted), or to a uniform that is

@@ -266,6 +266,32 @@ def test_tables_past_32_bits():
     assert (y[N - 1] == 3).all() and (y[65536] == 4).all()
 
 
+@pytest.mark.parametrize("N", [300, 9000])
+def test_what_a_workspace_holds_and_two_streams(N):
+    """The same gradient whatever workspace and output held, and from two calls
+    at once."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator().manual_seed(6)
+    V, H = 5000, 72
+    t, gy = tokens_of("heavy", N, V, g).cuda(), torch.randn(N, H, generator=g).bfloat16().cuda()
+    want = plp.embedding_bwd(gy, t, V)["grad_weight"]
+    for byte in (0x00, 0x01, 0x7f, 0xff):
+        ws = torch.full((1 << 26,), byte, dtype=torch.uint8, device="cuda")
+        out = torch.full((V, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+        plp.embedding_bwd(gy, t, V, workspace=ws, out={"grad_weight": out})
+        assert torch.equal(out, want), byte
+    sides, got = (torch.cuda.Stream(), torch.cuda.Stream()), []
+    for side in sides:
+        side.wait_stream(torch.cuda.current_stream())
+    for i in range(6):
+        with torch.cuda.stream(sides[i % 2]):
+            got.append(plp.embedding_bwd(gy, t, V)["grad_weight"])
+    for side in sides:
+        torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(x, want) for x in got)
+
+
 def test_streams_and_graphs():
     """On a stream of its own, and captured twice over separate memory and
     replayed in turn between eager calls."""

@@ -158,6 +158,28 @@ def test_clipped_norm_is_the_limit():
     assert abs(after - 2.5) <= 2.5 * (3 * U + 1e-6 / 100)
 
 
+@pytest.mark.parametrize("sizes", [[900, 0, 3000], [70001, 90000, 5] + [33] * 300], ids=len)
+def test_what_a_workspace_holds_and_two_streams(sizes):
+    """The same results whatever the workspace held, and from two calls at once."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    table = plp.grad_table(some(sizes, ["f32", "bf16", "f32"] * (len(sizes) // 3 + 1)))
+    run = lambda **kw: plp.grad_norm(table, max_norm=0.01, norms=True, **kw)  # noqa: E731
+    want = run()
+    same = lambda r: all(torch.equal(r[k], want[k]) for k in want)  # noqa: E731
+    for byte in (0x00, 0x7f, 0xff):
+        assert same(run(workspace=torch.full((1 << 20,), byte, dtype=torch.uint8, device="cuda"))), byte
+    sides, got = (torch.cuda.Stream(), torch.cuda.Stream()), []
+    for side in sides:
+        side.wait_stream(torch.cuda.current_stream())
+    for i in range(6):
+        with torch.cuda.stream(sides[i % 2]):
+            got.append(run())
+    for side in sides:
+        torch.cuda.current_stream().wait_stream(side)
+    assert all(map(same, got))
+
+
 def test_a_tensor_twice_and_overlap():
     require_gpu()
     import rl_policy_gradient_amd as plp

@@ -383,6 +383,42 @@ def test_batches_that_leave_rows_out(certain):
                 assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+@pytest.mark.parametrize("certain", [False, True])
+def test_what_a_workspace_holds_and_two_streams(certain):
+    """The same results whatever the workspace held, of batches that leave rows
+    out and of others, from two calls at once and from a captured graph."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    for B, K, V, s in ((700, 3, 600, dict(top_p=0.9)), (300, 4, 1500, dict(top_k=20)), (8, 3, 3000, dict()), (9, 0, 70, dict())):
+        z, tokens, u, q = (None if t is None else t.cuda() for t in inputs(B, K, V, "bf16", 78, certain=certain))
+        n = torch.randint(0, K + 1, (B,), generator=torch.Generator().manual_seed(2)).int().cuda()
+        kw = dict(s, draft_logits=q, num_drafts=n, **({} if q is None else {"draft_" + k: v for k, v in s.items()}))
+        want = check(z, tokens, u, q, n, s, s)
+        same = lambda r: all(torch.equal(r[k], want[k]) for k in want)  # noqa: E731
+        size = (B * (2 * K + 1) * ((V + 255) // 256 + 1) * 12 + B * ((2 * K + 1) * 40 + (K + 40) * 16 + V // 8)) + 65536
+        for byte in (0x00, 0x3f, 0x7f, 0xbf, 0xff):  # zeros, a half, large, minus a half, NaN
+            ws = torch.full((size,), byte, dtype=torch.uint8, device="cuda")
+            assert same(plp.verify_tokens(z, tokens, u, workspace=ws, **kw)), byte
+        sides, got = (torch.cuda.Stream(), torch.cuda.Stream()), []
+        for side in sides:
+            side.wait_stream(torch.cuda.current_stream())
+        for i in range(6):
+            with torch.cuda.stream(sides[i % 2]):
+                got.append(plp.verify_tokens(z, tokens, u, **kw))
+        for side in sides:
+            torch.cuda.current_stream().wait_stream(side)
+        assert all(map(same, got))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = plp.verify_tokens(z, tokens, u, **kw)
+        for _ in range(3):
+            for t in out.values():
+                t.fill_(7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert same(out) and same(plp.verify_tokens(z, tokens, u, **kw))
+
+
 def test_offsets_past_32_bits():
     require_gpu()
     B, K, V = 5, 1, 1000
