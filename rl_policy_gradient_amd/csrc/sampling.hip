@@ -78,7 +78,7 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
   u64* bq = reinterpret_cast<u64*>(lds + sizeof(Shared));
   float* bmax = reinterpret_cast<float*>(bq + G);
   uint16_t* act = reinterpret_cast<uint16_t*>(bmax + G);
-  Lists& ls = *reinterpret_cast<Lists*>(lds + shared_bytes(G));
+  Lists<>& ls = *reinterpret_cast<Lists<>*>(lds + shared_bytes(G));
   const int64_t row = blockIdx.x;
   const Row<T> r((const T*)a.logits + row * a.stride, a.V);
   const int nb = r.blocks();
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(NT) void sample_row_kernel(SampleArgs a, int G) {
                   uniform(min_p > 0.f ? fmin((double)min_p, 1.0) : -1.0)};
   const int per = (nb + NT - 1) / NT;  // blocks a thread takes, one after the other
   const int b0 = min(nb, (int)threadIdx.x * per), b1 = min(nb, b0 + per);
-  weigh_blocks(s, b0, b1);
+  weigh_blocks(s);
   u64 cut = 0;
   const bool limited = LIMITS && ((top_k > 0 && top_k < a.V) || top_p < 1.f || min_p > 0.f);
   if (limited) cut = s.cut(top_k, top_p, lowest_max);
@@ -181,7 +181,7 @@ hipError_t sample(const SampleArgs& a, hipStream_t st) {
         <<<dim3((G + kStatBlocks - 1) / kStatBlocks, (unsigned)b.N), kStatThreads, 0, st>>>(b, G);
     if (hipError_t e = hipGetLastError()) return e;
     if (a.top_k_rows || a.top_p_rows || a.min_p_rows || (a.top_k > 0 && a.top_k < a.V) || a.top_p < 1.f || a.min_p > 0.f)
-      sample_row_kernel<T, true><<<(unsigned)b.N, NT, shared_bytes(G) + sizeof(Lists), st>>>(b, G);
+      sample_row_kernel<T, true><<<(unsigned)b.N, NT, shared_bytes(G) + sizeof(Lists<>), st>>>(b, G);
     else
       sample_row_kernel<T, false><<<(unsigned)b.N, NT, shared_bytes(G), st>>>(b, G);
     if (hipError_t e = hipGetLastError()) return e;

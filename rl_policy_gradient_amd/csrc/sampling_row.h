@@ -246,14 +246,18 @@ __device__ __forceinline__ void block_stats(const typename Row<T>::Raw (&raw)[kS
 // one place in the code (unrolled and inlined where used it was 91 KB, and a
 // row took two to three times as long, fetching it).
 // ---------------------------------------------------------------------------
+// Threads of a row's workgroup: NT of them, one workgroup a CU, or where there
+// are more rows than CUs half as many and two a CU (verify.hip); no result
+// depends on which (TH, in what follows).
 constexpr int NT = 1024;
-constexpr int kWaves = NT / 64;
+constexpr int kHalfNT = NT / 2;
+constexpr int kWaves = NT / 64;  // at most
 constexpr int kBins = 2048;
-constexpr int kBinsPer = kBins / NT;
 constexpr int kList = 4096;        // logits that can be listed
 // Up to so many, every listed logit is compared with every other, else the
 // cut is searched for by histograms (51 listed: 18 us a call against 22).
-constexpr int kRanked = NT / 4;
+template <int TH>
+constexpr int kRanked = TH / 4;
 // Logits up to which a whole row is listed for top_k, when the maxima do not
 // bound it, instead of an estimate (64 rows, k = 50 to 400: of 300, 24 us
 // against 26; of 1000, 21 to 25 against 18 to 33; of 1500, 24 against 20).
@@ -298,14 +302,15 @@ __device__ __forceinline__ V_ wave_scan(V_ v) {
 
 // Sum over the threads before this one, and over all of them. `tmp` holds a
 // value per wave.
-template <typename V_>
+template <int TH = NT, typename V_>
 __device__ __forceinline__ V_ block_scan(V_ v, V_* tmp, V_& total) {
+  constexpr int waves_of = TH / 64;
   const V_ inc = wave_scan(v);
   const int wave = uniform((int)threadIdx.x >> 6);
   if ((threadIdx.x & 63) == 63) tmp[wave] = inc;
   __syncthreads();
-  const V_ waves = wave_scan(tmp[threadIdx.x & (kWaves - 1)]);  // the first kWaves lanes' count
-  total = lane_of(waves, kWaves - 1);
+  const V_ waves = wave_scan(tmp[threadIdx.x & (waves_of - 1)]);  // the first lanes' count
+  total = lane_of(waves, waves_of - 1);
   const V_ before = wave ? lane_of(waves, wave - 1) : (V_)0;
   __syncthreads();
   return before + (inc - v);
@@ -325,12 +330,29 @@ __device__ __forceinline__ void for_chunk(float (&z)[kChunk], F f) {
   }
 }
 
-struct Lists {  // for rows with limits only
+// For rows with limits only.
+template <int TH = NT>
+struct Lists {
   u64 list[kList];  // places
   u64 q[kList];     // their masses
   u64 mass[kBins];
   uint32_t count[kBins];
+  __device__ __forceinline__ u64* masses() { return q; }
 };
+// Two workgroups a CU have 80 KB of LDS each, up to some 440000 logits: the
+// masses of a short list, and what a pass puts side by side, are where the
+// histograms are at other times; a longer list's are formed again.
+template <>
+struct Lists<kHalfNT> {
+  u64 list[kList];
+  u64 mass[kBins];
+  uint32_t count[kBins];
+  __device__ __forceinline__ u64* masses() { return mass; }
+};
+static_assert(sizeof(Lists<kHalfNT>::mass) >= kHalfNT / kLanes * kSampleBlock * sizeof(float) &&
+                  sizeof(Lists<NT>::q) >= NT / kLanes * kSampleBlock * sizeof(float),
+              "a block's logits for each half wave");
+static_assert(kRanked<kHalfNT> <= kBins, "the masses of a short list");
 struct Shared {
   u64 scan64[kWaves];
   double scand[kWaves];
@@ -344,11 +366,13 @@ struct Shared {
   u64 place, a, b, bin_mass, above;
 };
 
-template <typename T>
+template <typename T, int TH = NT>
 struct RowSampler {
+  static constexpr int kBinsPer = kBins / TH;
+  static constexpr bool kMasses = TH == NT;  // whether a list's masses are kept
   const Row<T> r;
   Shared& sh;
-  Lists& ls;
+  Lists<TH>& ls;
   float* const bmax;    // [blocks] maxima
   u64* const bq;        // [blocks] the bits of the blocks' sums (doubles), later their kept masses
   uint16_t* const act;  // active blocks, by index
@@ -367,6 +391,13 @@ struct RowSampler {
   __device__ __forceinline__ u64 quant(double w) const {
     return (u64)__double_as_longlong(fma(w, unit, 0x1p52)) & 0xfffffffffffffull;
   }
+  // The mass of entry j of the list, which is `place`.
+  __device__ __forceinline__ u64 mass_of(int j, u64 place) const {
+    if constexpr (kMasses)
+      return ls.masses()[j];
+    else
+      return quant(weight(value_at(place)));
+  }
   __device__ __forceinline__ float value_at(u64 place) const {
     return Key<T>::value((uint32_t)(place >> kIndexBits));
   }
@@ -379,7 +410,7 @@ struct RowSampler {
     const float scale = (float)kBins / (mf - lowest_max);
     if (threadIdx.x == 0) sh.bin = -1;
     clear_bins();
-    for (int b = threadIdx.x; b < nb; b += NT) {
+    for (int b = threadIdx.x; b < nb; b += TH) {
       if (bmax[b] == -INFINITY) continue;
       const int bin = max(0, min(kBins - 1, (int)((bmax[b] - lowest_max) * scale)));
       atomicAdd(&ls.count[bin], 1u);
@@ -393,8 +424,8 @@ struct RowSampler {
       const int bin = kBins - 1 - ((int)threadIdx.x * kBinsPer + i);
       c += ls.count[bin], q += ls.mass[bin];
     }
-    c = block_scan(c, sh.scan32, tc);
-    if (!by_count) q = block_scan(q, sh.scan64, tq);
+    c = block_scan<TH>(c, sh.scan32, tc);
+    if (!by_count) q = block_scan<TH>(q, sh.scan64, tq);
     // a hundredth of a bin lower, so that a bin's rounding does not matter
     const auto value = [&](int bin) { return lowest_max + ((float)bin - 0.01f) / scale; };
     int best = -1;  // bins fall with the thread: the first to say yes has the highest
@@ -418,16 +449,16 @@ struct RowSampler {
   __device__ __forceinline__ bool peaked() {
     bool yes = false;
     const double most = S * fmax(1.0 / 32.0, fmin(4.0 / (double)nb, 0.5));
-    for (int b = threadIdx.x; b < nb; b += NT) yes |= __longlong_as_double((long long)bq[b]) >= most;
+    for (int b = threadIdx.x; b < nb; b += TH) yes |= __longlong_as_double((long long)bq[b]) >= most;
     return __syncthreads_or(yes ? 1 : 0) != 0;
   }
 
   // Lists the active blocks: those whose maximum is at least z.
   __device__ __forceinline__ int activate(float z) {
-    const int per = (nb + NT - 1) / NT, b0 = min(nb, (int)threadIdx.x * per), b1 = min(nb, b0 + per);
+    const int per = (nb + TH - 1) / TH, b0 = min(nb, (int)threadIdx.x * per), b1 = min(nb, b0 + per);
     uint32_t n = 0, total;
     for (int b = b0; b < b1; ++b) n += bmax[b] >= z;
-    uint32_t at = block_scan(n, sh.scan32, total);
+    uint32_t at = block_scan<TH>(n, sh.scan32, total);
     for (int b = b0; b < b1; ++b)
       if (bmax[b] >= z) act[at++] = (uint16_t)b;
     __syncthreads();
@@ -435,7 +466,7 @@ struct RowSampler {
   }
 
   __device__ __forceinline__ void begin_pass() {
-    for (int b = threadIdx.x; b < nb; b += NT) bq[b] = 0;
+    for (int b = threadIdx.x; b < nb; b += TH) bq[b] = 0;
     if (threadIdx.x == 0) sh.n = 0, sh.above = 0;
     __syncthreads();
   }
@@ -449,12 +480,12 @@ struct RowSampler {
   // sh.above), into bq what of it min_p keeps, and into the list the places of
   // those from zl on (sh.n of them; those past kList are only counted).
   __device__ __forceinline__ void pass(int nact, float zl, float zh) {
-    constexpr int step = NT / kLanes;
+    constexpr int step = TH / kLanes;
     begin_pass();
     u64 above = 0;
     const int lane = threadIdx.x % kLanes;
     // the half wave's logits above, in the place of the list's masses, which come later
-    float* const some = reinterpret_cast<float*>(ls.q) + threadIdx.x / kLanes * kSampleBlock;
+    float* const some = reinterpret_cast<float*>(ls.masses()) + threadIdx.x / kLanes * kSampleBlock;
     typename Row<T>::Raw next;
     int i = (int)threadIdx.x / kLanes;
     if (i < nact) next = r.fetch(act[i] * kLanes + lane);
@@ -524,7 +555,7 @@ struct RowSampler {
     u64 above = 0;
     const int lane = threadIdx.x % kLanes;
 #pragma unroll 1
-    for (int b = threadIdx.x / kLanes; b < nb; b += NT / kLanes) {
+    for (int b = threadIdx.x / kLanes; b < nb; b += TH / kLanes) {
       const int c = b * kLanes + lane, e0 = r.first(c);
       float z[kChunk];
       r.load(c, z);
@@ -562,19 +593,19 @@ struct RowSampler {
                                               bool whole, u64& cut, u64& through) {
     u64 mine = 0, total;
 #pragma unroll 1
-    for (int j = threadIdx.x; j < n; j += NT) {
+    for (int j = threadIdx.x; j < n; j += TH) {
       const u64 q = quant(weight(value_at(ls.list[j])));
-      ls.q[j] = q;
+      if (kMasses || n <= kRanked<TH>) ls.masses()[j] = q;
       mine += q;
     }
     u64 t = ~0ull;
-    if (n <= kRanked) {
+    if (n <= kRanked<TH>) {
       // every place against every other: four threads share one, each with a
       // quarter of the list
       const int e = threadIdx.x >> 2;
       const bool in = e < n;
       __syncthreads();
-      const u64 place = in ? ls.list[e] : 0, q = in ? ls.q[e] : 0;
+      const u64 place = in ? ls.list[e] : 0, q = in ? ls.masses()[e] : 0;
       uint32_t rank = 0;
       u64 before = 0;
       if (in)
@@ -582,7 +613,7 @@ struct RowSampler {
         for (int j = threadIdx.x & 3; j < n; j += 4) {
           const bool first = ls.list[j] > place;
           rank += first;
-          before += first ? ls.q[j] : 0;
+          before += first ? ls.masses()[j] : 0;
         }
       rank += permuted<0xb1, 0xf>(rank);
       rank += permuted<0x4e, 0xf>(rank);
@@ -605,7 +636,7 @@ struct RowSampler {
       cut = uniform(sh.place);
       through = uniform(sh.b);
     } else {
-      block_scan(mine, sh.scan64, total);
+      block_scan<TH>(mine, sh.scan64, total);
       total = uniform(total);
       u64 at = lo;  // the earliest cut so far
       through = above + total;
@@ -627,10 +658,10 @@ struct RowSampler {
       cut = at;  // or lo, the last place there can be: all of it
     }
 #pragma unroll 1
-    for (int j = threadIdx.x; j < n; j += NT) {
+    for (int j = threadIdx.x; j < n; j += TH) {
       const u64 place = ls.list[j];
       if (place >= cut && (least <= 0.0 || weight(value_at(place)) >= least))
-        atomicAdd(&bq[(index_at(place) + r.lead) / kSampleBlock], ls.q[j]);
+        atomicAdd(&bq[(index_at(place) + r.lead) / kSampleBlock], mass_of(j, place));
     }
     __syncthreads();
     return true;
@@ -650,8 +681,8 @@ struct RowSampler {
     }
     // by mass, the count above is not needed
     tc = 0;
-    if (!by_mass) c0 = an + block_scan(c0, sh.scan64, tc);
-    m0 = am + block_scan(m0, sh.scan64, tm);
+    if (!by_mass) c0 = an + block_scan<TH>(c0, sh.scan64, tc);
+    m0 = am + block_scan<TH>(m0, sh.scan64, tm);
     if (uniform(target > (by_mass ? am + tm : an + tc) ? 1 : 0)) return false;
 #pragma unroll
     for (int i = 0; i < kBinsPer; ++i) {
@@ -677,7 +708,7 @@ struct RowSampler {
   }
 
   __device__ __forceinline__ void clear_bins() {
-    for (int i = threadIdx.x; i < kBins; i += NT) ls.mass[i] = 0, ls.count[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += TH) ls.mass[i] = 0, ls.count[i] = 0;
     __syncthreads();
   }
   static __device__ __forceinline__ int shift_of(u64 range) {
@@ -695,10 +726,10 @@ struct RowSampler {
       const int shift = shift_of(hi - lo);
       clear_bins();
 #pragma unroll 1
-      for (int j = threadIdx.x; j < n; j += NT) {
+      for (int j = threadIdx.x; j < n; j += TH) {
         const u64 place = ls.list[j];
         if (place >= lo && place <= hi) {
-          atomicAdd(&ls.mass[(place - lo) >> shift], ls.q[j]);
+          atomicAdd(&ls.mass[(place - lo) >> shift], mass_of(j, place));
           atomicAdd(&ls.count[(place - lo) >> shift], 1u);
         }
       }
@@ -711,12 +742,12 @@ struct RowSampler {
     }
     // the few that are left, each against the others
 #pragma unroll 1
-    for (int j = threadIdx.x; j < n; j += NT) {
+    for (int j = threadIdx.x; j < n; j += TH) {
       const u64 place = ls.list[j];
       if (place >= lo && place <= hi) {
         const uint32_t at = atomicAdd(&sh.few, 1u);
         ls.mass[at] = place;
-        ls.mass[64 + at] = ls.q[j];
+        ls.mass[64 + at] = mass_of(j, place);
       }
     }
     __syncthreads();
@@ -749,7 +780,7 @@ struct RowSampler {
       clear_bins();
       const int chunks = r.chunks();
 #pragma unroll 1
-      for (int c = threadIdx.x; c < chunks; c += NT) {
+      for (int c = threadIdx.x; c < chunks; c += TH) {
         float z[kChunk];
         r.load(c, z);
         const int e0 = r.first(c);
@@ -788,7 +819,7 @@ struct RowSampler {
     clear_bins();
     float low = 0.f;
 #pragma unroll 1
-    for (int c = threadIdx.x * step; c < chunks; c += NT * step) {
+    for (int c = threadIdx.x * step; c < chunks; c += TH * step) {
       float z[kChunk];
       r.load(c, z);
 #pragma unroll
@@ -822,7 +853,7 @@ struct RowSampler {
       both[i] = (u64)fmin(mass[i] * fine, 0x1p32) << 20 | cnt[i];
       mine += both[i];
     }
-    u64 run = block_scan(mine, sh.scan64, all);
+    u64 run = block_scan<TH>(mine, sh.scan64, all);
     const uint32_t c0 = (uint32_t)run & 0xfffff;
     if (by_count) {
       const float aim = ((float)t + (step > 1 ? 4.f * sqrtf((float)t * (float)step) : 0.f)) / (float)step;
@@ -959,20 +990,21 @@ struct RowSampler {
 
 // Bytes of LDS before the lists. Every part begins at a multiple of its
 // elements' size: the lists at one of 16, the blocks' 8-byte sums after Shared.
-static_assert(alignof(Lists) <= 16 && alignof(Shared) <= 16 && sizeof(Shared) % sizeof(u64) == 0, "LDS alignment");
+static_assert(alignof(Lists<>) <= 16 && alignof(Shared) <= 16 && sizeof(Shared) % sizeof(u64) == 0, "LDS alignment");
 __host__ __device__ inline size_t shared_bytes(int G) {
   return (sizeof(Shared) + (size_t)G * (sizeof(u64) + sizeof(float) + sizeof(uint16_t)) + 15) / 16 * 16;
 }
 
 // The row's blocks from their statistics into LDS, and over them the largest
 // logit, the least finite maximum and whether any is NaN.
+template <int TH = NT>
 __device__ __forceinline__ void load_blocks(Shared& sh, float* bmax, u64* bq, const float* block_max,
                                             const double* block_sum, int nb, float& most, float& lowest_max, int& nan) {
   most = -INFINITY;
   lowest_max = INFINITY;
   nan = 0;
 #pragma unroll 1
-  for (int b = threadIdx.x; b < nb; b += NT) {
+  for (int b = threadIdx.x; b < nb; b += TH) {
     const float v = block_max[b];
     bmax[b] = v;
     bq[b] = (u64)__double_as_longlong(block_sum[b]);
@@ -990,10 +1022,11 @@ __device__ __forceinline__ void load_blocks(Shared& sh, float* bmax, u64* bq, co
   }
   if (threadIdx.x == 0) sh.block = 0x7fffffff, sh.bin = 0x7fffffff;
   __syncthreads();
-  static_assert(kWaves == 16, "a row of lanes holds the waves' values");
-  most = uniform(row_reduce(sh.maxw[threadIdx.x & (kWaves - 1)], Max()));
-  lowest_max = uniform(row_reduce(sh.minw[threadIdx.x & (kWaves - 1)], Min()));
-  nan = __ballot(sh.flag[threadIdx.x & (kWaves - 1)]) != 0;
+  constexpr int waves = TH / 64;
+  static_assert(waves <= 16, "a row of lanes holds the waves' values");
+  most = uniform(row_reduce(sh.maxw[threadIdx.x & (waves - 1)], Max()));
+  lowest_max = uniform(row_reduce(sh.minw[threadIdx.x & (waves - 1)], Min()));
+  nan = __ballot(sh.flag[threadIdx.x & (waves - 1)]) != 0;
   __syncthreads();
 }
 
@@ -1004,9 +1037,9 @@ __device__ __forceinline__ bool has_distribution(float most, int nan, float tau,
 }
 
 // The first of the largest logits: what it is is in sh.bin for every thread.
-template <typename T>
+template <int TH = NT, typename T>
 __device__ __forceinline__ void find_first(Shared& sh, const Row<T>& r, const float* bmax, float mf, int nb) {
-  for (int b = threadIdx.x; b < nb; b += NT)
+  for (int b = threadIdx.x; b < nb; b += TH)
     if (bmax[b] == mf) atomicMin(&sh.block, b);
   __syncthreads();
   const int e = sh.block * kSampleBlock - r.lead + (int)threadIdx.x;
@@ -1015,17 +1048,24 @@ __device__ __forceinline__ void find_first(Shared& sh, const Row<T>& r, const fl
 }
 
 // The blocks' sums relative to the row's largest logit, in bq, and over all
-// (s.S); this thread's are b0 .. b1 - 1.
-template <typename T>
-__device__ __forceinline__ void weigh_blocks(RowSampler<T>& s, int b0, int b1) {
-  double sum = 0.0;
+// (s.S). NT threads take some blocks each, which lie side by side, or TH the
+// parts of several of those: the sum is the same to the last bit.
+template <typename T, int TH>
+__device__ __forceinline__ void weigh_blocks(RowSampler<T, TH>& s) {
+  const int each = (s.nb + NT - 1) / NT;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    const double w = __longlong_as_double((long long)s.bq[b]) * s.weight(s.bmax[b]);
-    s.bq[b] = (u64)__double_as_longlong(w);
-    sum += w;
+  for (int t0 = 0; t0 < NT; t0 += TH) {
+    const int b0 = min(s.nb, (t0 + (int)threadIdx.x) * each), b1 = min(s.nb, b0 + each);
+    double sum = 0.0, all;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const double w = __longlong_as_double((long long)s.bq[b]) * s.weight(s.bmax[b]);
+      s.bq[b] = (u64)__double_as_longlong(w);
+      sum += w;
+    }
+    block_scan<TH>(sum, s.sh.scand, all);
+    s.S = t0 ? all + s.S : all;
   }
-  block_scan(sum, s.sh.scand, s.S);
   s.S = uniform(s.S);
   // q = round(w 2^F) add up to less than 2^52: S < 2^(e+1), and the roundings
   // add at most half of V <= 2^20

@@ -202,14 +202,14 @@ __device__ __forceinline__ void leave_row(const VerifyArgs& a, int per, const Dr
 // leaves them out (256 x 8 certain drafts at 32000, top_p 0.95: 84 us, 143 with
 // every row). Otherwise a sequence's rows follow each other (384 rows of 96 x 3
 // drafts: 47 us, 62 by their place).
-template <typename T, bool LIMITS>
-__global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, int G) {
+template <typename T, bool LIMITS, int TH>
+__global__ __launch_bounds__(TH, 4) void verify_row_kernel(VerifyArgs a, int per, int G) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   Shared& sh = *reinterpret_cast<Shared*>(lds);
   u64* bq = reinterpret_cast<u64*>(lds + sizeof(Shared));
   float* bmax = reinterpret_cast<float*>(bq + G);
   uint16_t* act = reinterpret_cast<uint16_t*>(bmax + G);
-  Lists& ls = *reinterpret_cast<Lists*>(lds + shared_bytes(G));
+  Lists<TH>& ls = *reinterpret_cast<Lists<TH>*>(lds + shared_bytes(G));
   __shared__ Drafted drafted;
   const Place at = place_of_group(a, blockIdx.x, per);
   if (!used(a, at)) return;
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, i
   float mf, lowest_max;
   int nan;
   if (a.skip && threadIdx.x == 0) sh.place = (u64)refused;
-  load_blocks(sh, bmax, bq, a.block_max + row * G, a.block_sum + row * G, nb, mf, lowest_max, nan);
+  load_blocks<TH>(sh, bmax, bq, a.block_max + row * G, a.block_sum + row * G, nb, mf, lowest_max, nan);
   if (a.skip && uniform(sh.place) < (u64)at.j) return;
   if (threadIdx.x == 0) drafted = Drafted{token, token >= 0 ? (float)r.p[token] : 0.f};
   if (!has_distribution(mf, nan, tau, top_p, min_p)) {
@@ -239,24 +239,22 @@ __global__ __launch_bounds__(NT) void verify_row_kernel(VerifyArgs a, int per, i
     return;
   }
   if (tau == 0.f) {
-    find_first(sh, r, bmax, mf, nb);
+    find_first<TH>(sh, r, bmax, mf, nb);
     if (threadIdx.x == 0)
       leave_row(a, per, drafted, VerifyRow{1.0, 1.0, mf, tau, -1.f, 0.f, sh.bin, kOneToken});
     return;
   }
-  RowSampler<T> s{r, sh, ls, bmax, bq, act, nb, mf, uniform((double)mf), uniform(rate_of(tau)),
+  RowSampler<T, TH> s{r, sh, ls, bmax, bq, act, nb, mf, uniform((double)mf), uniform(rate_of(tau)),
                   uniform(least_of(tau)), 0.0, 0.0,
                   uniform(min_p > 0.f ? fmin((double)min_p, 1.0) : -1.0)};
-  const int each = (nb + NT - 1) / NT;
-  const int b0 = min(nb, (int)threadIdx.x * each), b1 = min(nb, b0 + each);
-  weigh_blocks(s, b0, b1);
+  weigh_blocks(s);
   VerifyRow out{s.S, s.S, mf, tau, -1.f, -INFINITY, -1, kWeights};
   if (LIMITS && ((top_k > 0 && top_k < a.V) || top_p < 1.f || min_p > 0.f)) {
     const u64 cut = s.cut(top_k, top_p, lowest_max);
     u64 mine = 0, total;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += bq[b];
-    block_scan(mine, sh.scan64, total);
+    for (int b = threadIdx.x; b < nb; b += TH) mine += bq[b];
+    block_scan<TH>(mine, sh.scan64, total);
     out = VerifyRow{(double)total / s.unit, s.S, mf, tau, (float)s.least, s.value_at(cut), index_at(cut), kWeights};
   }
   if (threadIdx.x == 0) leave_row(a, per, drafted, out);
@@ -575,6 +573,22 @@ VerifyRows from(const VerifyRows& r, int64_t seq, size_t esize) {
   return o;
 }
 
+// Rows up to which each has a CU and its workgroup all threads it can have;
+// above, half of them, and two workgroups a CU. At 151936 bf16 and top_p 0.95
+// 24 x 4 drafts (216 rows) take 103 us with all, 115 with half; 32 x 4 (288 rows)
+// 160 and 143; at 32000 256 x 4 284 and 218. (A quarter of the threads, two a CU
+// all the same for what their lists take of its LDS: 242.)
+constexpr unsigned kFewRows = 256;
+
+template <typename T, int TH>
+hipError_t row_kernel(const VerifyArgs& a, int per, int G, unsigned rows, bool limits, hipStream_t st) {
+  if (limits)
+    verify_row_kernel<T, true, TH><<<rows, TH, shared_bytes(G) + sizeof(Lists<TH>), st>>>(a, per, G);
+  else
+    verify_row_kernel<T, false, TH><<<rows, TH, shared_bytes(G), st>>>(a, per, G);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t verify(const VerifyArgs& all, hipStream_t st) {
   const int G = sample_blocks(all.V), blocks = verify_blocks(all.V);
@@ -602,11 +616,9 @@ hipError_t verify(const VerifyArgs& all, hipStream_t st) {
       const unsigned rows = (unsigned)(a.B * ((to - from + 1) * places - (places == 2 && to == a.K ? 1 : 0)));
       verify_stats_kernel<T><<<dim3((G + kStatBlocks - 1) / kStatBlocks, rows), kStatThreads, 0, st>>>(a, per, G);
       if (hipError_t e = hipGetLastError()) return e;
-      if (limits)
-        verify_row_kernel<T, true><<<rows, NT, shared_bytes(G) + sizeof(Lists), st>>>(a, per, G);
-      else
-        verify_row_kernel<T, false><<<rows, NT, shared_bytes(G), st>>>(a, per, G);
-      if (hipError_t e = hipGetLastError()) return e;
+      hipError_t e = rows > kFewRows ? row_kernel<T, kHalfNT>(a, per, G, rows, limits, st)
+                                     : row_kernel<T, NT>(a, per, G, rows, limits, st);
+      if (e) return e;
     }
     // some 2048 workgroups, of whole sets of blocks
     const int sets = (blocks + kRestBlocks - 1) / kRestBlocks;

@@ -383,6 +383,32 @@ def test_batches_that_leave_rows_out(certain):
                 assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [700, 9000, 140000, 300000])
+def test_a_sequence_does_not_depend_on_the_batch(V, dtype):
+    """A batch of more rows than CUs, whose workgroups are smaller, against its
+    sequences a few at a time: the same bits."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator(device="cuda").manual_seed(V)
+    B, K, few = 63, 2, 21
+    for flat in (False, True):
+        z = torch.randn(B, K + 1, V, generator=g, device="cuda") * (0.3 if flat else 3.0)
+        q = (z[:, :K] + 0.3 * torch.randn(B, K, V, generator=g, device="cuda")).to(DT[dtype])
+        z = z.to(DT[dtype])
+        u = torch.rand(B, K + 1, generator=g, device="cuda")
+        for s in (dict(), dict(top_p=0.9), dict(top_p=0.3, temperature=0.7), dict(top_k=50), dict(top_k=3000, top_p=0.8),
+                  dict(min_p=0.1), dict(top_k=400, min_p=0.001, temperature=1.5)):
+            drafts = torch.stack([plp.sample_tokens(q[:, k], torch.rand(B, generator=g, device="cuda"), **s)["token"]
+                                  for k in range(K)], 1)
+            kw = dict(s, **{"draft_" + k: v for k, v in s.items()})
+            whole = plp.verify_tokens(z, drafts, u, draft_logits=q, **kw)
+            assert (whole["tokens"][:, 0] >= 0).all()
+            for b in range(0, B, few):
+                part = plp.verify_tokens(z[b:b + few], drafts[b:b + few], u[b:b + few], draft_logits=q[b:b + few], **kw)
+                assert all(torch.equal(part[k], whole[k][b:b + few]) for k in part), (s, b)
+
+
 @pytest.mark.parametrize("certain", [False, True])
 def test_what_a_workspace_holds_and_two_streams(certain):
     """The same results whatever the workspace held, of batches that leave rows
