@@ -24,11 +24,11 @@
 //
 // What bounds them: the first by operations in fp64, as in sampling (576 rows of
 // 151936 bf16: 77 us, their bytes 30); the second by the length of a row's chain
-// of steps on one CU where there are limits (15 us for 9 rows of 151936, 50 for
-// 384 of 32000 with settings of their own, a round and a half of the 256 CUs),
-// 8 without; the third by fp64 again (64 x 2 rows of 151936: 24 us), and 5 for
-// one sequence, three loads one after the other; the last by two of them, 5 to
-// 6. 1 x 4 drafts at 151936 bf16 take 29 us, 64 x 4 105 without limits.
+// of steps on a CU, or half of one, where there are limits (15 us for 9 rows of
+// 151936, 43 for some 400 of 32000 with settings of their own), 7 without; the
+// third by fp64 again (64 x 2 rows of 151936: 24 us), and 5 for one sequence,
+// three loads one after the other; the last by two of them, 5 to 6. 1 x 4 drafts
+// at 151936 bf16 take 29 us, 64 x 4 104 without limits.
 #include "sampling_row.h"
 #include "verify_ops.h"
 
@@ -197,11 +197,9 @@ __device__ __forceinline__ void leave_row(const VerifyArgs& a, int per, const Dr
 
 // What sampling's row kernel finds before it draws. With `skip` rows go by their
 // place in the sequence, the first of all sequences first (a target's row, then
-// the draft's): a launch of many more rows than run at once (one a CU, with
+// the draft's): a launch of many more rows than run at once (two a CU, with
 // limits) then meets many whose sequence has a draft refused before them, and
-// leaves them out (256 x 8 certain drafts at 32000, top_p 0.95: 84 us, 143 with
-// every row). Otherwise a sequence's rows follow each other (384 rows of 96 x 3
-// drafts: 47 us, 62 by their place).
+// leaves them out. Otherwise a sequence's rows follow each other.
 template <typename T, bool LIMITS, int TH>
 __global__ __launch_bounds__(TH, 4) void verify_row_kernel(VerifyArgs a, int per, int G) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -548,17 +546,28 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int block
   }
 }
 
-// Rows of a launch above which they look at what is refused before them: some
-// four a CU, of which one runs at once; one a CU where drafts are certain, whose
-// rows need not look at each other (640 rows of 128 x 4 at 32000: 89 us, 105
-// without; with the draft's logits 576 rows take the same either way).
+// Rows with limits above which they look at what is refused before them: twice
+// as many as run at once (certain drafts at 32000, top_p 0.95: 1280 rows of 256
+// x 4 113 us, 126 without; 2000 of 400 x 4 158 and 193; with the draft's logits
+// 1800 of 200 x 4 171 and 179; up to a thousand the same either way, but 672 of 96
+// x 3 of ragged numbers 74 in their sequences' order and 78 by their place).
 constexpr unsigned kSkipRows = 1024;
 
-// Rows from which a sequence's first go ahead of the others, whose statistics
-// are then left out too (2304 rows of 256 x 8 certain drafts at 32000: 134 us
-// against 142; 2560 of 512 x 4: 168 against 192; but 640 of 128 x 4: 103 against
-// 89; with the draft's logits the same).
-constexpr int64_t kPhaseRows = 2048;
+// Launches over rows, so that the statistics of those after a refused draft are
+// left out too: the sequences' first rows, then the others, or their first, the
+// second and the others. It costs some 7 us a launch and pays by the logits, of
+// which certain drafts, mostly refused at once, leave out more (without limits in
+// one, two and three: 64 x 4 drafts at 151936 110, 117 and 123 us, 128 x 4 195,
+// 187 and 189, 256 x 4 369, 332 and 319, 512 x 8 at 32000 301, 277 and 265, 512 x
+// 4 certain ones at 32000 115, 93 and 93), and where rows have limits by their
+// number too (certain drafts at 32000, top_p 0.95: 2304 rows of 256 x 8 158, 141
+// and 150, 1280 of 256 x 4 113 and 122; 1000 of 200 x 4 at 151936 319, 255 and 282).
+constexpr int64_t kStepRows = 2048, kStepLogits = (int64_t)1 << 27;
+int steps_of(int64_t rows, int V, bool limits, bool certain) {
+  const int64_t logits = rows * V * (certain ? 2 : 1);
+  if (logits > 2 * kStepLogits) return certain ? 2 : 3;
+  return (limits ? rows > kStepRows : logits > kStepLogits) ? 2 : 1;
+}
 
 bool limited(const VerifyRows& r, int V) {
   return r.top_k_seq || r.top_p_seq || r.min_p_seq || (r.top_k > 0 && r.top_k < V) || r.top_p < 1.f || r.min_p > 0.f;
@@ -607,11 +616,11 @@ hipError_t verify(const VerifyArgs& all, hipStream_t st) {
     a.accepted = all.accepted + s0;
     if (all.logp) a.logp = all.logp + s0 * (all.K + 1);
     if (all.kept_logp) a.kept_logp = all.kept_logp + s0 * (all.K + 1);
-    a.skip = limits && a.B * per > (all.of[1].logits ? kSkipRows : kSkipRows / 4);
-    // all rows at once, or the first of each sequence and then the others
-    const int places = all.of[1].logits ? 2 : 1;
+    const int places = all.of[1].logits ? 2 : 1, steps = steps_of(a.B * per, a.V, limits, places == 1);
+    a.skip = steps > 1 || (limits && a.B * per > kSkipRows);
+    // all rows at once, or the first of each sequence, its second and so on and then the others
     for (int from = 0, to; from <= a.K; from = to + 1) {
-      to = a.skip && a.B * per > kPhaseRows && from == 0 ? 0 : a.K;
+      to = std::min(a.K, from < steps - 1 ? from : a.K);
       a.slot = from * places;
       const unsigned rows = (unsigned)(a.B * ((to - from + 1) * places - (places == 2 && to == a.K ? 1 : 0)));
       verify_stats_kernel<T><<<dim3((G + kStatBlocks - 1) / kStatBlocks, rows), kStatThreads, 0, st>>>(a, per, G);

@@ -373,7 +373,7 @@ def test_batches_that_leave_rows_out(certain):
     """So many rows with limits that those after a refused draft are left out, in
     an order that changes with the launch: the same bits at every call."""
     require_gpu()
-    for B, K, V in ((300, 4, 1500), (700, 3, 600)):
+    for B, K, V in ((300, 4, 1500), (700, 3, 600), (150, 2, 1000)):
         z, tokens, u, q = inputs(B, K, V, "bf16", 77, certain=certain)
         n = torch.randint(0, K + 1, (B,), generator=torch.Generator().manual_seed(1)).int()
         for s in (dict(top_p=0.9), dict(top_k=20, temperature=0.7)):
@@ -407,6 +407,42 @@ def test_a_sequence_does_not_depend_on_the_batch(V, dtype):
             for b in range(0, B, few):
                 part = plp.verify_tokens(z[b:b + few], drafts[b:b + few], u[b:b + few], draft_logits=q[b:b + few], **kw)
                 assert all(torch.equal(part[k], whole[k][b:b + few]) for k in part), (s, b)
+
+
+@pytest.mark.parametrize("certain,B,K,V", [(True, 2200, 1, 40000), (True, 230, 2, 110000), (False, 240, 1, 200000),
+                                           (False, 260, 3, 160000)])
+def test_rows_in_several_launches(certain, B, K, V):
+    """So many logits that a sequence's first rows, or its first and its second,
+    go ahead of the others: as a few sequences at a time, and as a graph."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator(device="cuda").manual_seed(B)
+    z = (torch.randn(B, K + 1, V, generator=g, device="cuda") * 3).bfloat16()
+    q = None if certain else (z[:, :K].float() + 0.5 * torch.randn(B, K, V, generator=g, device="cuda")).bfloat16()
+    n = torch.randint(0, K + 1, (B,), generator=g, device="cuda").int()
+    u = torch.rand(B, K + 1, generator=g, device="cuda")
+    for s in (dict(), dict(top_p=0.9, min_p=0.001)):
+        drafts = torch.stack([plp.sample_tokens((z if certain else q)[:, k], torch.rand(B, generator=g, device="cuda"), **s)["token"]
+                              for k in range(K)], 1)
+        side = {} if certain else dict(draft_logits=q, **{"draft_" + k: v for k, v in s.items()})
+        whole = plp.verify_tokens(z, drafts, u, num_drafts=n, **s, **side)
+        assert (whole["tokens"][:, 0] >= 0).all() and (whole["accepted"] <= n).all()
+        for b in range(0, B, 10):
+            c = slice(b, b + 10)
+            if not certain:
+                side["draft_logits"] = q[c]
+            part = plp.verify_tokens(z[c], drafts[c], u[c], num_drafts=n[c], **s, **side)
+            assert all(torch.equal(part[k], whole[k][c]) for k in part), (s, b)
+        if not certain:
+            side["draft_logits"] = q
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = plp.verify_tokens(z, drafts, u, num_drafts=n, **s, **side)
+        for _ in range(3):
+            out["tokens"].fill_(7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(out[k], whole[k]) for k in out)
 
 
 @pytest.mark.parametrize("certain", [False, True])
