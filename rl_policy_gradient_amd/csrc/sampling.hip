@@ -64,7 +64,8 @@ __global__ __launch_bounds__(kStatThreads) void sample_stats_kernel(SampleArgs a
   fetch_block(r, b, lane, raw);
   float m;
   double s;
-  block_stats<T>(raw, temperature_of(a, row), m, s);
+  const float tau = temperature_of(a, row);
+  block_stats<T>(raw, tau, rate_of(tau), m, s);
   if (lane == 0) {
     a.block_max[row * G + b] = m;
     a.block_sum[row * G + b] = s;

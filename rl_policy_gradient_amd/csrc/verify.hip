@@ -23,12 +23,12 @@
 // token.
 //
 // What bounds them: the first by operations in fp64, as in sampling (576 rows of
-// 151936 bf16: 77 us, their bytes 30); the second by the length of a row's chain
+// 151936 bf16: 67 us, their bytes 30); the second by the length of a row's chain
 // of steps on a CU, or half of one, where there are limits (15 us for 9 rows of
 // 151936, 43 for some 400 of 32000 with settings of their own), 7 without; the
 // third by fp64 again (64 x 2 rows of 151936: 24 us), and 5 for one sequence,
 // three loads one after the other; the last by two of them, 5 to 6. 1 x 4 drafts
-// at 151936 bf16 take 29 us, 64 x 4 104 without limits.
+// at 151936 bf16 take 29 us, 64 x 4 96 without limits.
 #include "sampling_row.h"
 #include "verify_ops.h"
 
@@ -89,7 +89,13 @@ __global__ __launch_bounds__(kStatThreads) void verify_stats_kernel(VerifyArgs a
   fetch_block(r, b, lane, raw);
   float m;
   double s;
-  block_stats<T>(raw, src.tau_seq ? src.tau_seq[at.seq] : src.tau, m, s);
+  float tau = src.tau;
+  double rate = src.rate;  // (576 rows of 151936: a division in each thread took 4 us more)
+  if (src.tau_seq) {
+    tau = src.tau_seq[at.seq];
+    rate = rate_of(tau);
+  }
+  block_stats<T>(raw, tau, rate, m, s);
   if (lane == 0) {
     a.block_max[row * G + b] = m;
     a.block_sum[row * G + b] = s;
@@ -574,6 +580,7 @@ bool limited(const VerifyRows& r, int V) {
 }
 VerifyRows from(const VerifyRows& r, int64_t seq, size_t esize) {
   VerifyRows o = r;
+  o.rate = rate_of(r.tau);
   if (r.logits) o.logits = (const char*)r.logits + seq * r.seq_stride * (int64_t)esize;
   if (r.tau_seq) o.tau_seq = r.tau_seq + seq;
   if (r.top_p_seq) o.top_p_seq = r.top_p_seq + seq;

@@ -14,6 +14,7 @@ struct VerifyRows {
   int64_t seq_stride, row_stride;
   float tau, top_p, min_p;
   int top_k;
+  double rate;  // of the temperature, where that is one for all: the launcher's
   const float *tau_seq, *top_p_seq, *min_p_seq;  // instead of the scalars, or NULL
   const int32_t* top_k_seq;
 };
