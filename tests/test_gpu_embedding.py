@@ -124,6 +124,36 @@ def test_backward_of_many_tokens(N, H, V, kind, accumulate):
     check_bwd(tokens_of(kind, N, V, g), gy, V, 1.0, torch.float32, accumulate)
 
 
+def tokens_of_a_range(N, H, dtype):
+    """How many sorted tokens a wave adds up (embed_bwd_plan): ranges of 48 and
+    more do not fit a wave's lanes with what lies around them, and go 64 at a time."""
+    lanes = 64 * (4 if dtype == "f32" else 8)
+    most = max(1, 8192 // -(-H // lanes))
+    return max(8, -(-N // most))
+
+
+@pytest.mark.parametrize("kind", ["zipf", "heavy", "padded", "uniform", "falling"])
+@pytest.mark.parametrize("N,H,V", [(385024, 8, 20000), (385025, 8, 20000), (400000, 8, 50000), (1000000, 8, 1023),
+                                   (200000, 521, 9000)])
+def test_backward_of_long_ranges(N, H, V, kind):
+    """Ranges of 47 tokens, the longest that are taken at once, and of 48, 49 and
+    123, with rows of many lengths that cross their ends: of some 8 tokens (50000
+    rows), 20 (20000) and a thousand (1023). The last has slices of columns."""
+    require_gpu()
+    assert tokens_of_a_range(N, H, "bf16") == {385024: 47, 385025: 48, 400000: 49, 1000000: 123, 200000: 49}[N]
+    g = torch.Generator().manual_seed(N)
+    t, x = tokens_of(kind, N, V, g), torch.randn(N, H, generator=g)
+    if H == 521:
+        assert tokens_of_a_range(N, H, "f32") == 74  # three slices, the last of 9 columns
+        check_bwd(t, x.bfloat16(), V, 1.0, torch.float32, kind != "heavy")
+        if kind == "heavy":
+            check_bwd(t, x, V, 1.0, torch.float32, True)
+        return
+    for types in (("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")):
+        for accumulate in (False, True):
+            check_bwd(t, x.to(DT[types[0]]), V, 3.3, DT[types[1]], accumulate)
+
+
 def test_same_bits_at_every_call():
     require_gpu()
     import rl_policy_gradient_amd as plp
