@@ -154,6 +154,50 @@ def test_backward_of_long_ranges(N, H, V, kind):
             check_bwd(t, x.to(DT[types[0]]), V, 3.3, DT[types[1]], accumulate)
 
 
+@pytest.mark.parametrize("N,H", [(2 ** 25 + 5, 1), (2 ** 25 // 3 + 9, 1025)])
+def test_forward_of_several_launches(N, H):
+    """More rows than one launch takes: their last rows are another launch's, of
+    one slice of columns and of three (23 GB)."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    slices, V = -(-H // 512), 5000
+    assert -(-N // 4) * slices > 2 ** 23
+    g = torch.Generator(device="cuda").manual_seed(H)
+    w = torch.randn(V, H, generator=g, device="cuda").bfloat16()
+    t = torch.randint(-3, V + 3, (N,), generator=g, device="cuda")
+    buf = torch.full((N * H + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = plp.embedding_fwd(t, w, out={"y": buf[:N * H].view(N, H)})["y"]
+    for n in range(0, N, 2 ** 20):
+        some = t[n:n + 2 ** 20]
+        want = torch.where(((some >= 0) & (some < V))[:, None], w[some.clamp(0, V - 1)], 0.0)
+        assert torch.equal(y[n:n + 2 ** 20], want), n
+    assert (buf[N * H:] == 7).all()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("V", [2 ** 30 + 3, 2 ** 31 - 1])
+def test_four_passes_of_the_sort(V, accumulate):
+    """Tables of more than 2^30 rows, whose tokens differ in each of four digits."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    N, H = 5000, 1
+    g = torch.Generator().manual_seed(7)
+    near = torch.tensor([0, 2 ** 8, 2 ** 16, 2 ** 24, 2 ** 30, V - 40])[torch.randint(0, 6, (N,), generator=g)]
+    t = near + torch.randint(0, 40, (N,), generator=g)  # some past V - 1 where V - 40 is near 2^30 already
+    t[::50], t[1::50], t[2] = -1, V, V - 1
+    gy = torch.randn(N, H, generator=g).bfloat16()
+    gw = torch.full((V, H), 0.5 if accumulate else float("nan"), dtype=torch.bfloat16, device="cuda")
+    plp.embedding_bwd(gy.cuda(), t.cuda(), V, accumulate=accumulate, out={"grad_weight": gw})
+    ids, short = torch.unique(t[(t >= 0) & (t < V)], return_inverse=True)
+    assert ids[-1] == V - 1 and len(ids) > 150
+    old = torch.full((len(ids), H), 0.5, dtype=torch.bfloat16) if accumulate else None
+    want, off, _ = reference(short, gy[(t >= 0) & (t < V)], len(ids), 1.0, old)
+    got = gw[ids.cuda()].cpu().double()
+    assert ((got - want).abs() <= off + HALF[torch.bfloat16] * (want.abs() + off)).all()
+    gw[ids.cuda()] = 0.5 if accumulate else 0.0
+    assert all((part == (0.5 if accumulate else 0.0)).all() for part in gw.view(-1).split(2 ** 28))
+
+
 def test_same_bits_at_every_call():
     require_gpu()
     import rl_policy_gradient_amd as plp
