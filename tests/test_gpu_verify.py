@@ -271,6 +271,25 @@ def test_tokens_are_distributed_as_the_targets(certain):
     assert (count > 0).any() and (count == 0).any()
 
 
+def test_the_token_after_a_certain_draft_is_distributed_as_the_targets():
+    """Whether a sequence has a second token depends on the first draft and its
+    uniform; what it is on the second draft, its uniform and the last one, which
+    are independent of those: so it is distributed as p_1, its draft taken or not."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    B, K, V = 200000, 2, 6
+    g = torch.Generator().manual_seed(5)
+    z, q = torch.randn(1, K + 1, V, generator=g), torch.randn(1, K, V, generator=g)
+    p = torch.softmax(z[0].double(), -1)
+    draft = torch.multinomial(torch.softmax(q[0], -1), B, replacement=True, generator=g).t().contiguous()
+    r = plp.verify_tokens(z.cuda().expand(B, K + 1, V), draft.cuda(), torch.rand(B, K + 1, generator=g).cuda())
+    tokens, count = r["tokens"].cpu(), r["accepted"].cpu()
+    for k in range(K + 1):
+        seen = tokens[count >= k, k]
+        n, got = len(seen), torch.bincount(seen, minlength=V).double()
+        assert n > 1000 and ((got - n * p[k]).abs() <= 5 * (n * p[k] * (1 - p[k])).sqrt()).all(), (k, got / n, p[k])
+
+
 def test_drafts_that_are_no_token():
     require_gpu()
     z, tokens, u, q = inputs(40, 3, 500, "f32", 21)
