@@ -488,10 +488,13 @@ typedef struct plp_verify_args {
  * then distributed as one drawn from p. (Where p_k - q_k is nowhere above zero,
  * as for a draft that neither side could give, it is drawn from p_k.) A draft
  * outside [0,V) is refused. Rows past the sequence's num_drafts are not read.
- * Probabilities are formed in 64 bits, good to about 1e-13 of themselves (one
- * below 2^-1000 of the row's largest is 0); sums in an order that goes by V, so
- * a sequence's result does not depend on the others, and on its place in memory
- * only where a border lies within that of a uniform. A sequence that comes to a
+ * Probabilities are formed in 64 bits, good to about 1e-13 of themselves, or
+ * where limits apply to V 2^-51 (7e-11 at 151936), as the kept mass is
+ * plp_sample_tokens' sum of rounded weights; one below 2^-1000 of the row's
+ * largest is 0, while one that plp_sample_tokens' rounding makes nothing keeps
+ * its chance. Sums are added in an order that goes by V, so a sequence's result
+ * does not depend on the others, and on its place in memory only where a border
+ * lies within 1e-13 of a uniform. A sequence that comes to a
  * row without a distribution (plp_sample_tokens says which; the target's, or the
  * draft's of a draft that all before were accepted), or to a uniform that is
  * NaN, ends there with token -1 and NaN log-probs. Uniforms outside [0,1) are

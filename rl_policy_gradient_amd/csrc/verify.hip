@@ -11,10 +11,17 @@
 // it had been drawn from p.
 //
 // Probabilities are weights in fp64 (to 2e-14, by sampling's exponential) over
-// masses that are exact or good to 1e-13; sums are added in an order that goes
-// by V alone, in blocks of 256 logits from the row's first. What is accepted
-// and which token is drawn can so change only where a border lies within about
-// 1e-13 of a uniform number.
+// masses. A whole row's mass is a sum in fp64, good to 1e-13 of itself. A limited
+// row's is sampling's sum of whole numbers, each within 2^-51 of the whole mass
+// of its weight, equal logits all on the same side; k tokens of V are kept that
+// hold k / V of the whole or more, so that it is good to V 2^-51 of itself (7e-11
+// at 151936, where one token and 151935 equal ones are off by 4e-11). Weights of
+// less than half a unit are none of that mass, but have their chance here, as
+// all have down to 2^-1000 of the largest. What is left is added in fp64, in an
+// order that goes by V alone, in blocks of 256 logits from the row's first. What
+// is accepted and which token is drawn can so differ from the exact
+// probabilities' only where a border lies that close to a uniform number, and
+// with the row's place in memory only within 1e-13 of one.
 //
 // Four launches: the statistics of every row's blocks, as in sampling; the
 // rows' cuts and masses, and from them the chances of the drafted token; the

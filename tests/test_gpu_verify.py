@@ -290,6 +290,61 @@ def test_the_token_after_a_certain_draft_is_distributed_as_the_targets():
         assert n > 1000 and ((got - n * p[k]).abs() <= 5 * (n * p[k] * (1 - p[k])).sqrt()).all(), (k, got / n, p[k])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,tail,limits", [(151936, -13.0, dict(top_p=0.9999)), (151936, -13.0, dict(min_p=1e-12)),
+                                           (151936, -20.0, dict(min_p=1e-12)), (151936, -20.0, dict(top_k=100000)),
+                                           (1 << 20, -20.0, dict(min_p=1e-12)), (1 << 20, -24.0, dict(top_k=1000000))])
+def test_masses_of_long_tails(V, tail, limits, dtype):
+    """One likely token and all others equal, whose weights are all rounded the
+    same way: a limited row's mass is a sum of weights that are each off by up to
+    2^-51 of the whole mass, k of the V in all by up to k 2^-51 of it, of which the
+    largest k hold k / V at least; the log of a mass is off by as much of itself:
+    V 2^-51. The mass is sampling's to the last bit."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    B, K, top = 3, 1, V // 2
+    z = torch.full((B, K + 1, V), tail).to(DT[dtype])
+    z[:, :, top] = 0.0
+    tokens, u = torch.tensor([[top], [top], [5]]), torch.tensor([[0.125, 0.0], [0.125, 0.25], [0.5, 0.25]])
+    r = plp.verify_tokens(z.cuda(), tokens.cuda(), u.cuda(), **limits)
+    settings = tuple({**dict(zip(NAMES, (1.0, 0, 1.0, 0.0))), **limits}[k] for k in NAMES)
+    settings = (settings[0], settings[1], float(np.float32(settings[2])), float(np.float32(settings[3])))
+    for b in range(B):
+        want = reference(z[b].double().numpy(), None, tokens[b].numpy(), u[b].double().numpy(), K, settings, None)
+        assert r["accepted"][b] == want[1] == (b < 2)
+        assert np.array_equal(r["tokens"][b].cpu().numpy(), want[0])
+        for name, w, off in (("logp", want[2], 0.0), ("kept_logp", want[3], V * 2.0 ** -51)):
+            got = r[name][b].double().cpu().numpy()
+            assert (np.abs(got - w) <= U * np.abs(w) + off + 1e-12).all(), (b, name, got, w)
+    one = plp.sample_tokens(z[:2, K].cuda(), u[:2, K].cuda().contiguous(), **limits)
+    assert torch.equal(r["tokens"][:2, K], one["token"]) and torch.equal(r["kept_logp"][:2, K], one["kept_logp"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_tokens_that_weigh_next_to_nothing(dtype):
+    """A token has its chance down to 2^-1000 (e^-693.1) of the row's largest, also
+    where sampling's rounding of the weights leaves nothing of it; below there is none."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    logits = [-36.0, -40.0, -300.0, -692.0, -696.0, -700.0]
+    B, K, V = 2, len(logits), 300
+    for s in (dict(), dict(top_k=200)):
+        z = torch.full((B, K + 1, V), -800.0)
+        z[:, :, 7] = 0.0
+        tokens = torch.arange(10, 10 + K).expand(B, K).contiguous()
+        for k, x in enumerate(logits):
+            z[:, k, 10 + k] = x
+        u = torch.tensor([0.0, 0.5])[:, None].expand(B, K + 1).contiguous()
+        r = plp.verify_tokens(z.to(DT[dtype]).cuda(), tokens.cuda(), u.cuda(), **s)
+        assert r["accepted"].tolist() == [4, 0]
+        assert r["tokens"].tolist() == [[10, 11, 12, 13, 7, -1, -1], [7] + [-1] * K]
+        # each log-prob is z - log(1 + e^x), x the row's drafted logit, e^x at most e^-36 =
+        # 2.3e-16 (not 0): a value good to 1e-12 like the others, and one rounding
+        want = torch.tensor([logits[:4] + [0.0] * 3, [0.0] * (K + 1)], dtype=torch.float64)
+        for name in ("logp", "kept_logp"):
+            assert ((r[name].cpu().double() - want).abs() <= U * want.abs() + 1e-12).all(), (name, r[name])
+
+
 def test_drafts_that_are_no_token():
     require_gpu()
     z, tokens, u, q = inputs(40, 3, 500, "f32", 21)
