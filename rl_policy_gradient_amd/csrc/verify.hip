@@ -35,7 +35,7 @@
 // 151936, 43 for some 400 of 32000 with settings of their own), 7 without; the
 // third by fp64 again (64 x 2 rows of 151936: 24 us), and 5 for one sequence,
 // three loads one after the other; the last by two of them, 5 to 6. 1 x 4 drafts
-// at 151936 bf16 take 29 us, 64 x 4 96 without limits.
+// at 151936 bf16 take 29 us, 64 x 4 93 to 106 without limits.
 #include "sampling_row.h"
 #include "verify_ops.h"
 
@@ -561,25 +561,35 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int block
 
 // Rows with limits above which they look at what is refused before them: twice
 // as many as run at once (certain drafts at 32000, top_p 0.95: 1280 rows of 256
-// x 4 113 us, 126 without; 2000 of 400 x 4 158 and 193; with the draft's logits
-// 1800 of 200 x 4 171 and 179; up to a thousand the same either way, but 672 of 96
-// x 3 of ragged numbers 74 in their sequences' order and 78 by their place).
+// x 4 110 us, 123 without; 2000 of 400 x 4 150 and 184; with the draft's logits
+// 1800 of 200 x 4 165 and 174; up to a thousand the same either way, but 672 of 96
+// x 3 of ragged numbers 74 in their sequences' order and 80 by their place).
 constexpr unsigned kSkipRows = 1024;
 
 // Launches over rows, so that the statistics of those after a refused draft are
 // left out too: the sequences' first rows, then the others, or their first, the
 // second and the others. It costs some 7 us a launch and pays by the logits, of
 // which certain drafts, mostly refused at once, leave out more (without limits in
-// one, two and three: 64 x 4 drafts at 151936 110, 117 and 123 us, 128 x 4 195,
-// 187 and 189, 256 x 4 369, 332 and 319, 512 x 8 at 32000 301, 277 and 265, 512 x
-// 4 certain ones at 32000 115, 93 and 93), and where rows have limits by their
-// number too (certain drafts at 32000, top_p 0.95: 2304 rows of 256 x 8 158, 141
-// and 150, 1280 of 256 x 4 113 and 122; 1000 of 200 x 4 at 151936 319, 255 and 282).
+// one, two and three: 64 x 4 drafts at 151936 105, 109 and 116 us, 128 x 4 178,
+// 172 and 177, 256 x 4 342, 308 and 293 to 304, 512 x 8 at 32000 277, 256 and 245;
+// 256 x 4 certain ones at 32000 60, 56 and 63, 512 x 4 114, 90 and 91; with limits, top_p
+// 0.95: 64 x 4 drafts at 151936 228, 238 and 286, 128 x 4 389, 378 and 408, 256 x 4
+// 653, 641 and 624, 200 x 4 certain ones 322, 243 and 275). With limits a launch
+// ends with its last rows' cuts, beside which other rows had been at work: by
+// their number it pays for certain drafts alone (at 32000 in one and two: 1280
+// rows of 256 x 4 108 and 120, 2000 of 400 x 4 150 and 146, 2560 of 512 x 4 192 and
+// 171, with top_k 50 155 and 135, 2560 of 256 x 9 156 and 141; of ragged numbers,
+// on average half of the rows, 2304 of 256 x 8 117 and 122, 2700 138 and 137), and
+// not for those with logits (2304 rows of 256 x 4 204 and 212, with top_k 50 158 and
+// 163, 3600 294 and 307, 2800 of 400 x 3 in fp32 with settings of each 174 and 199,
+// 11900 of 700 x 8 at 5000 371 and 380), which go by the logits (512 x 4 at 32000,
+// 147 million: 372 and 367; ragged ones in fp32, 600 x 3, 134 million just above
+// the border: 239 and 261).
 constexpr int64_t kStepRows = 2048, kStepLogits = (int64_t)1 << 27;
 int steps_of(int64_t rows, int V, bool limits, bool certain) {
   const int64_t logits = rows * V * (certain ? 2 : 1);
   if (logits > 2 * kStepLogits) return certain ? 2 : 3;
-  return (limits ? rows > kStepRows : logits > kStepLogits) ? 2 : 1;
+  return (limits && certain ? rows > kStepRows : logits > kStepLogits) ? 2 : 1;
 }
 
 bool limited(const VerifyRows& r, int V) {
@@ -598,8 +608,8 @@ VerifyRows from(const VerifyRows& r, int64_t seq, size_t esize) {
 
 // Rows up to which each has a CU and its workgroup all threads it can have;
 // above, half of them, and two workgroups a CU. At 151936 bf16 and top_p 0.95
-// 24 x 4 drafts (216 rows) take 103 us with all, 115 with half; 32 x 4 (288 rows)
-// 160 and 143; at 32000 256 x 4 284 and 218. (A quarter of the threads, two a CU
+// 24 x 4 drafts (216 rows) take 102 us with all, 114 with half; 28 x 4 (252 rows)
+// 111 and 121; 32 x 4 (288 rows) 160 and 143; at 32000 256 x 4 279 and 216. (A quarter of the threads, two a CU
 // all the same for what their lists take of its LDS: 242.)
 constexpr unsigned kFewRows = 256;
 
