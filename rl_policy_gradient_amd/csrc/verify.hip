@@ -563,7 +563,9 @@ __global__ __launch_bounds__(NT) void verify_pick_kernel(VerifyArgs a, int block
 // as many as run at once (certain drafts at 32000, top_p 0.95: 1280 rows of 256
 // x 4 110 us, 123 without; 2000 of 400 x 4 150 and 184; with the draft's logits
 // 1800 of 200 x 4 165 and 174; up to a thousand the same either way, but 672 of 96
-// x 3 of ragged numbers 74 in their sequences' order and 80 by their place).
+// x 3 of ragged numbers 74 in their sequences' order and 80 by their place. Under
+// settings of each sequence it pays less: 400 x 8 certain ones 206 and 281, 700 x 8
+// with logits 634 and 799, but 256 x 4 of these at 151936 512 and 480).
 constexpr unsigned kSkipRows = 1024;
 
 // Launches over rows, so that the statistics of those after a refused draft are
@@ -572,29 +574,34 @@ constexpr unsigned kSkipRows = 1024;
 // which certain drafts, mostly refused at once, leave out more (without limits in
 // one, two and three: 64 x 4 drafts at 151936 105, 109 and 116 us, 128 x 4 178,
 // 172 and 177, 256 x 4 342, 308 and 293 to 304, 512 x 8 at 32000 277, 256 and 245;
-// 256 x 4 certain ones at 32000 60, 56 and 63, 512 x 4 114, 90 and 91; with limits, top_p
-// 0.95: 64 x 4 drafts at 151936 228, 238 and 286, 128 x 4 389, 378 and 408, 256 x 4
-// 653, 641 and 624, 200 x 4 certain ones 322, 243 and 275). With limits a launch
-// ends with its last rows' cuts, beside which other rows had been at work: by
-// their number it pays for certain drafts alone (at 32000 in one and two: 1280
-// rows of 256 x 4 108 and 120, 2000 of 400 x 4 150 and 146, 2560 of 512 x 4 192 and
-// 171, with top_k 50 155 and 135, 2560 of 256 x 9 156 and 141; of ragged numbers,
-// on average half of the rows, 2304 of 256 x 8 117 and 122, 2700 138 and 137), and
-// not for those with logits (2304 rows of 256 x 4 204 and 212, with top_k 50 158 and
-// 163, 3600 294 and 307, 2800 of 400 x 3 in fp32 with settings of each 174 and 199,
-// 11900 of 700 x 8 at 5000 371 and 380), which go by the logits (512 x 4 at 32000,
-// 147 million: 372 and 367; ragged ones in fp32, 600 x 3, 134 million just above
-// the border: 239 and 261).
+// 256 x 4 certain ones at 32000 60, 56 and 63, 512 x 4 114, 90 and 91). With limits
+// a launch ends with its last rows' cuts, beside which other rows had been at
+// work. Under one setting for all it pays past twice as many logits (256 x 4 at
+// 151936, top_p 0.95: 653, 641 and 624, with top_k 50 384, 350 and 337, 700 x 8 at
+// 32000 766, 741 and 728; 200 x 4 certain ones at 151936 322, 243 and 275), before
+// by the rows of certain drafts (at 32000: 1280 of 256 x 4 108 and 120, 2000 of 400 x
+// 4 150 and 146, 2560 of 512 x 4 192 and 171, with top_k 50 155 and 135; of ragged
+// numbers, on average half of the rows, 2304 of 256 x 8 117 and 122, 2700 138 and
+// 137) and by both where the drafts have logits (at 32000: 2304 rows of 256 x 4 204
+// and 212, 3600 294 and 307, but 4608 372 and 367, 7200 587 and 577; 120 x 4 at
+// 151936 in fp32 375 and 383). Under settings of each sequence, whose cuts take
+// more or less long, it does not where they have (256 x 4 drafts at 151936 534, 597
+// and 674, in fp32 and ragged 395, 449 and 515, 100 x 4 180 and 232, 400 x 3 at
+// 32000 174 and 199; 700 x 8 665, 652 and 648), and for certain ones by their rows
+// alone (200 x 4 at 151936 270, 295 and 329, 512 x 4 at 32000 191, 190 and 205, 400 x
+// 8 219, 205 and 218).
 constexpr int64_t kStepRows = 2048, kStepLogits = (int64_t)1 << 27;
-int steps_of(int64_t rows, int V, bool limits, bool certain) {
+int steps_of(int64_t rows, int V, bool limits, bool each, bool certain) {
   const int64_t logits = rows * V * (certain ? 2 : 1);
-  if (logits > 2 * kStepLogits) return certain ? 2 : 3;
-  return (limits && certain ? rows > kStepRows : logits > kStepLogits) ? 2 : 1;
+  if (logits > 2 * kStepLogits && !(limits && each)) return certain ? 2 : 3;
+  if (!limits) return logits > kStepLogits ? 2 : 1;
+  return rows > kStepRows && (certain || (logits > kStepLogits && !each)) ? 2 : 1;
 }
 
 bool limited(const VerifyRows& r, int V) {
   return r.top_k_seq || r.top_p_seq || r.min_p_seq || (r.top_k > 0 && r.top_k < V) || r.top_p < 1.f || r.min_p > 0.f;
 }
+bool of_each(const VerifyRows& r) { return r.tau_seq || r.top_k_seq || r.top_p_seq || r.min_p_seq; }
 VerifyRows from(const VerifyRows& r, int64_t seq, size_t esize) {
   VerifyRows o = r;
   o.rate = rate_of(r.tau);
@@ -627,6 +634,7 @@ hipError_t verify(const VerifyArgs& all, hipStream_t st) {
   const int G = sample_blocks(all.V), blocks = verify_blocks(all.V);
   const int per = verify_rows(all.K, all.of[1].logits != nullptr);
   const bool limits = limited(all.of[0], all.V) || (all.of[1].logits && limited(all.of[1], all.V));
+  const bool each_own = of_each(all.of[0]) || (all.of[1].logits && of_each(all.of[1]));
   const int64_t most = std::max(1, 32768 / per);  // the grid's second dimension holds 65535
   for (int64_t s0 = 0; s0 < all.B; s0 += most) {
     VerifyArgs a = all;
@@ -640,7 +648,7 @@ hipError_t verify(const VerifyArgs& all, hipStream_t st) {
     a.accepted = all.accepted + s0;
     if (all.logp) a.logp = all.logp + s0 * (all.K + 1);
     if (all.kept_logp) a.kept_logp = all.kept_logp + s0 * (all.K + 1);
-    const int places = all.of[1].logits ? 2 : 1, steps = steps_of(a.B * per, a.V, limits, places == 1);
+    const int places = all.of[1].logits ? 2 : 1, steps = steps_of(a.B * per, a.V, limits, each_own, places == 1);
     a.skip = steps > 1 || (limits && a.B * per > kSkipRows);
     // all rows at once, or the first of each sequence, its second and so on and then the others
     for (int from = 0, to; from <= a.K; from = to + 1) {

@@ -519,6 +519,35 @@ def test_rows_in_several_launches(certain, B, K, V):
             assert all(torch.equal(out[k], whole[k]) for k in out)
 
 
+@pytest.mark.parametrize("certain,B,K,V", [(False, 260, 3, 160000), (True, 230, 2, 200000), (False, 900, 2, 700),
+                                           (True, 900, 2, 700), (True, 60, 3, 700)])
+def test_settings_of_each_sequence_in_large_batches(certain, B, K, V):
+    """Large batches whose sequences have settings of their own, in one launch over
+    rows or several, against their sequences a few at a time: the same bits."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator(device="cuda").manual_seed(B + V)
+    z = (torch.randn(B, K + 1, V, generator=g, device="cuda") * 3).bfloat16()
+    q = None if certain else (z[:, :K].float() + 0.5 * torch.randn(B, K, V, generator=g, device="cuda")).bfloat16()
+    n, u = (torch.randint(0, K + 1, (B,), generator=g, device="cuda").int(), torch.rand(B, K + 1, generator=g, device="cuda"))
+    pick = lambda v, t: torch.tensor(v, dtype=t, device="cuda")[  # noqa: E731
+        torch.randint(0, len(v), (B,), generator=g, device="cuda")]
+    s = dict(temperature=pick([0.0, 0.7, 1.0, 1.3], torch.float32), top_k=pick([0, 0, 20, 400], torch.int32),
+             top_p=pick([1.0, 0.9, 0.99], torch.float32), min_p=pick([0.0, 0.0, 0.05], torch.float32))
+    drafts = torch.stack([plp.sample_tokens((z if certain else q)[:, k], torch.rand(B, generator=g, device="cuda"), **s)["token"]
+                          for k in range(K)], 1)
+
+    def some(c):
+        side = {} if certain else dict(draft_logits=q[c], **{"draft_" + k: v[c] for k, v in s.items()})
+        return plp.verify_tokens(z[c], drafts[c], u[c], num_drafts=n[c], **{k: v[c] for k, v in s.items()}, **side)
+
+    whole = some(slice(None))
+    assert (whole["tokens"][:, 0] >= 0).all() and (whole["accepted"] <= n).all()
+    for b in range(0, B, 20):
+        part = some(slice(b, b + 20))
+        assert all(torch.equal(part[k], whole[k][b:b + 20]) for k in part), b
+
+
 @pytest.mark.parametrize("certain", [False, True])
 def test_what_a_workspace_holds_and_two_streams(certain):
     """The same results whatever the workspace held, of batches that leave rows
