@@ -26,7 +26,10 @@
 // that wrote every row once, zeros where a merge of tokens and rows had none,
 // took 108: the sort, which only latency bounds, came before all of it. 16384
 // rows of 4096 fp32 into 32000: 150 (5.3 TB/s). Into a gradient that is there:
-// 512 rows 14 (the call from Python; 3.6, 7.1 and 3.6 on the device), 65536 70.
+// 512 rows 14 to 15, its three launches' latency (3.6 the sort, 7.2 the adding's
+// loads one after another, 3.6 a join of little), 65536 70 (their bytes 36: the
+// gradient's row is loaded with each of its tokens, of which the last one's is
+// used). Narrow rows leave lanes without columns: 65536 of 64 bf16 49, as of 128.
 #include "training_ops.h"
 
 #include <algorithm>
