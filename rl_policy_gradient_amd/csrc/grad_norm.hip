@@ -8,7 +8,8 @@
 // Squares are formed and added in fp64: a square of an fp32 or bf16 value is
 // exact there (24 + 24 bits of 53) and neither over- nor underflows, so a norm
 // is good to half a step of fp32 whatever the gradients' size. Two launches: a
-// workgroup a tile (at most some 4096 in all) leaves the tile's sum, then one
+// workgroup a tile (each tensor's last may be short, an empty one's is empty: at
+// most 4096 and the list's length in all) leaves the tile's sum, then one
 // workgroup adds the tiles' sums in a fixed order, and others those of a tensor
 // each, where asked for. A short list takes one launch of one workgroup.
 //

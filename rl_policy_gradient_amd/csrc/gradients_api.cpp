@@ -46,7 +46,9 @@ size_t carve_embed_bwd(void* ws, EmbedBwd& a) {
 constexpr int64_t kMaxGradNumel = (int64_t)1 << 40;
 constexpr int kMaxGrads = 1 << 20;
 // Elements of a tile, log2: at least 2048 (a load of 16 bytes a thread for
-// bf16), and at most some 4096 tiles for the finishing workgroup to add.
+// bf16), and at most 4096 tiles and one a tensor for the finishing workgroup to
+// add (20000 tensors 7 us, 200000 42: little beside the launches that sum them, of
+// up to 240 tensors each, which take 0.85 ms for 20000).
 constexpr int kMinTileShift = 11;
 constexpr int64_t kMostTiles = 4096;
 
