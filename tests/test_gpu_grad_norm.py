@@ -82,6 +82,28 @@ def test_many_tensors(count):
         assert torch.equal(a, (b.float() * out["scale"]).to(b.dtype))
 
 
+@pytest.mark.parametrize("count,most", [(4096, 5), (5000, 0), (20000, 9), (20000, 700)])
+def test_long_lists(count, most):
+    """More tensors than a list of few has tiles, most of them of a few elements or
+    none: every tensor's norm, the whole one, and the clipping in place."""
+    require_gpu()
+    import rl_policy_gradient_amd as plp
+    g = torch.Generator().manual_seed(count + most)
+    sizes = torch.randint(0, most + 1, (count,), generator=g)
+    flat = torch.randn(int(sizes.sum()), generator=g).to(DT["bf16" if most == 9 else "f32"])
+    grads = list(flat.cuda().split(sizes.tolist()))
+    table = plp.grad_table(grads)
+    out = plp.grad_norm(table, max_norm=0.25, norms=True)
+    own = torch.zeros(count, dtype=torch.float64).index_add_(0, torch.arange(count).repeat_interleave(sizes), flat.double().square())
+    assert out["norms"].shape == (count,)
+    got, want = out["norms"].cpu().double(), own.sqrt()
+    assert ((got - want).abs() <= U * want * (1 + 1e-6) + 1e-13 * want).all()
+    norm = math.sqrt(math.fsum(own.tolist()))
+    assert near(float(out["norm"]), norm) and near(float(out["scale"]), min(1.0, 0.25 / (norm + 1e-6)))
+    plp.clip_grads(table, out["scale"])
+    assert torch.equal(torch.cat(grads).cpu(), (flat.float() * out["scale"].cpu()).to(flat.dtype))
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("more", [-1, 0, 1])
 def test_around_what_one_workgroup_takes(more, kind):
