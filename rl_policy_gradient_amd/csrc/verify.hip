@@ -616,8 +616,9 @@ VerifyRows from(const VerifyRows& r, int64_t seq, size_t esize) {
 // Rows up to which each has a CU and its workgroup all threads it can have;
 // above, half of them, and two workgroups a CU. At 151936 bf16 and top_p 0.95
 // 24 x 4 drafts (216 rows) take 102 us with all, 114 with half; 28 x 4 (252 rows)
-// 111 and 121; 32 x 4 (288 rows) 160 and 143; at 32000 256 x 4 279 and 216. (A quarter of the threads, two a CU
-// all the same for what their lists take of its LDS: 242.)
+// 111 and 121; 32 x 4 (288 rows) 160 and 143; at 32000 256 x 4 279 and 216. (A
+// quarter of the threads, two a CU all the same for what their lists take of its
+// LDS: 242.)
 constexpr unsigned kFewRows = 256;
 
 template <typename T, int TH>
